@@ -10,7 +10,8 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "combine.hip"]
+SOURCES = ["api.hip", "layout.hip", "dispatch.hip", "combine.hip", "experts_api.hip", "experts.hip", "rows_quant.hip",
+           "combine_grad.hip"]
 LIB = os.path.join(HERE, "libmoe_get.so")
 # write-pattern probes the benchmark times next to the dispatch (not part of libmoe_get)
 PROBE_SOURCES = ["hbm_probe.hip"]

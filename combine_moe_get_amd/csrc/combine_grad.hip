@@ -1,0 +1,190 @@
+// combine_grad.hip -- the gradient of the weighted combine.
+//
+// out[t] = sum_j w[t,j] Moe_j(t) (combine.hip), so with g the gradient of out[t]:
+//   routed slot     grad of its row: w g;   of w: <g, row>
+//   copy slot       grad of x: += w g;      of w: <g, x>
+//   constant slot   grad of x: += w alpha1 g; of w: <g, alpha1 x + alpha2 v>;
+//                   alpha1 += w g x, alpha2 += w g v, v += w g alpha2 (all element-wise, over all tokens)
+//   zero, dropped or masked slot: nothing; w: 0
+// One workgroup a token: g is read once, every expert row once and every gradient row is written once.
+// The gradients of the constant experts' vectors are sums over tokens: a second kernel, one workgroup per
+// (expert, 64 columns), whose waves each take every sixteenth part of the slots in order and are added in
+// order, so that the result does not depend on the launch.
+#include "experts_internal.hpp"
+
+namespace moe {
+
+__device__ __forceinline__ uint32_t pack2g(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ void unpack8g(const u32x4 &v, float *f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(v[i]);
+    f[2 * i + 1] = bf16_hi(v[i]);
+  }
+}
+
+enum : int { G_NONE = 0, G_ROUTED = 1, G_COPY = 2, G_CONST = 3 };
+
+template <int KMAX, int THREADS>
+__global__ void __launch_bounds__(THREADS) combine_grad_kernel(CombineGradArgs a) {
+  const CombineArgs &c = a.c;
+  __shared__ float part[THREADS / 64][KMAX];
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int H = c.H, K = c.K, nch = H >> 3;
+  const bool live = !c.mask || c.mask[t];
+
+  int kind[KMAX], row[KMAX];  // row: of expert_out, or of the constant experts' vectors
+  float w[KMAX], dot[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    kind[j] = G_NONE;
+    row[j] = 0;
+    w[j] = dot[j] = 0.0f;
+    if (j < K && live) {
+      const int id = c.topk_idx[(size_t)t * K + j];
+      w[j] = c.w[(size_t)t * K + j];
+      const int zc = c.E + c.Z;
+      if (id >= 0 && id < c.E) {
+        row[j] = c.dst_row[(size_t)t * K + j];
+        kind[j] = row[j] >= 0 ? G_ROUTED : G_NONE;
+      } else if (id >= zc && id < zc + c.C) {
+        kind[j] = G_COPY;
+      } else if (id >= zc + c.C && id < zc + c.C + c.Kc) {
+        kind[j] = G_CONST;
+        row[j] = id - zc - c.C;
+      }
+    }
+  }
+  for (int ch = tid; ch < nch; ch += THREADS) {
+    float g[8], x[8], gx[8];
+    unpack8g(((const u32x4 *)(a.go + (size_t)t * H))[ch], g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gx[e] = x[e] = 0.0f;
+    if (c.ori_x) unpack8g(((const u32x4 *)(c.ori_x + (size_t)t * H))[ch], x);
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (kind[j] == G_NONE) continue;
+      float y[8];
+      if (kind[j] == G_ROUTED) {
+        const size_t at = (size_t)row[j] * nch + ch;
+        if (a.gw) unpack8g(((const u32x4 *)c.y)[at], y);
+        if (a.gy) {
+          u32x4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = pack2g(w[j] * g[2 * e], w[j] * g[2 * e + 1]);
+          ((u32x4 *)a.gy)[at] = o;
+        }
+      } else if (kind[j] == G_COPY) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = x[e];
+          gx[e] = __builtin_fmaf(w[j], g[e], gx[e]);
+        }
+      } else {
+        float a1[8], a2[8], v[8];
+        const size_t at = (size_t)row[j] * nch + ch;
+        unpack8g(((const u32x4 *)c.a1)[at], a1);
+        unpack8g(((const u32x4 *)c.a2)[at], a2);
+        unpack8g(((const u32x4 *)c.cv)[at], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = __builtin_fmaf(a1[e], x[e], a2[e] * v[e]);
+          gx[e] = __builtin_fmaf(w[j] * a1[e], g[e], gx[e]);
+        }
+      }
+      if (a.gw) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(g[e], y[e], dot[j]);
+      }
+    }
+    if (a.gx) {
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = pack2g(gx[2 * e], gx[2 * e + 1]);
+      ((u32x4 *)(a.gx + (size_t)t * H))[ch] = o;
+    }
+  }
+  if (a.gw) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+#pragma unroll
+      for (int s = 32; s > 0; s >>= 1) dot[j] += __shfl_xor(dot[j], s);
+      if (lane == 0) part[wave][j] = dot[j];
+    }
+    __syncthreads();
+    if (tid < K) {
+      float s = 0.0f;
+      for (int v = 0; v < THREADS / 64; ++v) s += part[v][tid];
+      a.gw[(size_t)t * K + tid] = s;
+    }
+  }
+}
+
+// workgroup (64 columns, constant expert): 16 waves, wave v adds the slots of the v-th sixteenth of the tokens
+__global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
+  const CombineArgs &c = a.c;
+  __shared__ float sg[16][64], sq[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = blockIdx.y, h = blockIdx.x * 64 + lane;
+  const int id = c.E + c.Z + c.C + k;
+  const int per = (c.T + 15) / 16, lo = wave * per, hi = lo + per < c.T ? lo + per : c.T;
+  float g = 0.0f, q = 0.0f;
+  for (int64_t s0 = (int64_t)lo * c.K; s0 < (int64_t)hi * c.K; s0 += 64) {
+    const int64_t s = s0 + lane;
+    const bool in = s < (int64_t)hi * c.K;
+    bool hit = in && c.topk_idx[s] == id;
+    if (hit && c.mask) hit = c.mask[s / c.K] != 0;
+    const float w = hit ? c.w[s] : 0.0f;
+    uint64_t hits = ballot(hit);
+    while (hits) {
+      const int l = __builtin_ctzll(hits);
+      hits &= hits - 1;
+      if (h < c.H) {
+        const int64_t at = (s0 + l) / c.K * c.H + h;
+        const float wg = readlane_f(w, l) * __uint_as_float((uint32_t)a.go[at] << 16);
+        g += wg;
+        if (a.ga1) q = __builtin_fmaf(wg, __uint_as_float((uint32_t)c.ori_x[at] << 16), q);
+      }
+    }
+  }
+  sg[wave][lane] = g;
+  sq[wave][lane] = q;
+  __syncthreads();
+  if (wave == 0 && h < c.H) {
+    for (int v = 1; v < 16; ++v) {
+      g += sg[v][lane];
+      q += sq[v][lane];
+    }
+    const size_t at = (size_t)k * c.H + h;
+    if (a.ga1) a.ga1[at] = q;
+    if (a.ga2) a.ga2[at] = __uint_as_float((uint32_t)c.cv[at] << 16) * g;
+    if (a.gv) a.gv[at] = __uint_as_float((uint32_t)c.a2[at] << 16) * g;
+  }
+}
+
+template <int KMAX>
+static void launch_k(const CombineGradArgs &a, hipStream_t st) {
+  hipLaunchKernelGGL((combine_grad_kernel<KMAX, 256>), dim3((unsigned)a.c.T), dim3(256), 0, st, a);
+}
+
+hipError_t launch_combine_grad(const CombineGradArgs &a, hipStream_t st) {
+  if (a.c.T > 0 && (a.gy || a.gw || a.gx)) {
+    if (a.c.K <= 1) launch_k<1>(a, st);
+    else if (a.c.K <= 2) launch_k<2>(a, st);
+    else if (a.c.K <= 4) launch_k<4>(a, st);
+    else if (a.c.K <= 8) launch_k<8>(a, st);
+    else launch_k<16>(a, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.c.Kc > 0 && (a.ga1 || a.ga2 || a.gv))  // T = 0: zeros
+    hipLaunchKernelGGL(const_grad_kernel, dim3((unsigned)((a.c.H + 63) / 64), (unsigned)a.c.Kc), dim3(1024), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -277,6 +277,106 @@ int moe_combine_capped(const moe_get_shape_t *shape, int32_t max_workgroups, con
                        const int32_t *dst_row, const uint16_t *ori_x, const uint16_t *const_alpha1,
                        const uint16_t *const_alpha2, const uint16_t *const_v, uint16_t *out, void *stream);
 
+/* ---- the expert stage: products grouped by expert, their gradients, row quantization ----------
+ *
+ * What the caller does with the received rows between dispatch and combine (y = experts(expand_x)),
+ * and the way back through it.  The rows of expert e are the ones the layout gave it: compact
+ * (rank_stride 0) rows [expert_offsets[e], expert_offsets[e + 1]); with fixed per-rank windows
+ * (rank_stride A) the same number of rows from r*A + expert_offsets[e] - expert_offsets[r L] on, r = e / L,
+ * cut at the end of the window.  How many rows each expert has is read on the device: any number,
+ * none included.  Rows of no expert (behind the last, or behind a window's last) are neither read
+ * nor written.  Offsets that do not ascend, or that pass `rows`, are cut to the buffers: nothing
+ * outside them is touched, and what the rows then hold is unspecified. */
+typedef struct moe_experts_shape {
+  int64_t rows;          /* rows the row buffers hold: 0 <= rows < 2^31 */
+  int64_t rank_stride;   /* 0: compact rows; A > 0: windows of A rows, num_ranks * A <= rows */
+  int32_t num_experts;   /* 1..2048, a multiple of num_ranks */
+  int32_t num_ranks;     /* >= 1 */
+  int32_t in_features;   /* elements of a row that goes in: 1..65536 */
+  int32_t out_features;  /* elements of a row that comes out: a multiple of 8, 8..65536 */
+} moe_experts_shape_t;
+
+/* Types of rows and weights. */
+#define MOE_ROWS_BF16 0   /* bf16; in_features a multiple of 8 */
+#define MOE_ROWS_INT8 1   /* int8 codes with one fp32 scale a row (as moe_dispatch sends them); in_features % 16 == 0 */
+#define MOE_ROWS_MXFP4 2  /* microscaled 4-bit floats; in_features % 32 == 0.  Two e2m1 codes a byte, the
+                             even element low; one e8m0 scale byte s (2^(s - 127), 255: NaN) per 32 elements */
+
+/* What is done to the sums before they are rounded to bf16. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_SWIGLU 1  /* out = silu(g) * u: the weights hold 2 * out_features rows an expert, first those of g */
+
+/* Validate an experts shape for rows of a type (MOE_ROWS_*). */
+int moe_experts_check_shape(const moe_experts_shape_t *shape, int32_t row_type);
+
+/* out[r, n] = act( sum_k x[r, k] w[e][n, k] ), e the expert of row r.
+ *  row_type           MOE_ROWS_*: the type of x and of w
+ *  act                MOE_ACT_*
+ *  in  x [rows, in_features]                  bf16 / int8 / packed e2m1 ([rows, in_features / 2] bytes)
+ *  in  row_scales     INT8: float32 [rows] or NULL (all ones); MXFP4: uint8 [rows, in_features / 32];
+ *                     BF16: NULL
+ *  in  w [num_experts, Nw, in_features]       of x's type; Nw = out_features, twice that with MOE_ACT_SWIGLU
+ *  in  w_scales       INT8: float32 [num_experts, Nw] or NULL (all ones);
+ *                     MXFP4: uint8 [num_experts, Nw, in_features / 32]; BF16: NULL
+ *  in  expert_offsets [num_experts + 1] int32 from the layout
+ *  out out [rows, out_features] bf16
+ * BF16: products exact, summed in fp32.  INT8: summed exactly in int32, then scaled by the row's and
+ * the output channel's scale in fp32.  MXFP4: blocks of 32 products scaled by both powers of two and
+ * summed in fp32; a NaN scale makes every sum it enters NaN.  The activation works on the fp32 values;
+ * one rounding to bf16 at the end.  x, w and out must be 16-byte aligned, float32 scales 4-byte.
+ * Results do not depend on the launch (no atomics; the order of each sum is fixed by the shape). */
+int moe_experts_matmul(const moe_experts_shape_t *shape, int32_t row_type, int32_t act, const void *x,
+                       const void *row_scales, const void *w, const void *w_scales, const int32_t *expert_offsets,
+                       uint16_t *out, void *stream);
+
+/* Gradient of the bf16 product (MOE_ACT_NONE) to its rows:
+ * grad_x[r, k] = sum_n grad_out[r, n] w[e][n, k], fp32 sums, rounded once.
+ *  in  grad_out [rows, out_features] bf16, w [num_experts, out_features, in_features] bf16
+ *  out grad_x [rows, in_features] bf16 */
+int moe_experts_matmul_dgrad(const moe_experts_shape_t *shape, const uint16_t *grad_out, const uint16_t *w,
+                             const int32_t *expert_offsets, uint16_t *grad_x, void *stream);
+
+/* Gradient of the bf16 product to its weights:
+ * grad_w[e][n, k] = sum over the rows r of e of grad_out[r, n] x[r, k], fp32 sums, rounded at most once.
+ * Every element is written: zeros for an expert without rows.
+ *  in  grad_out [rows, out_features] bf16, x [rows, in_features] bf16
+ *  out grad_w [num_experts, out_features, in_features], bf16 (grad_w_fp32 0) or float32 (grad_w_fp32 1) */
+int moe_experts_matmul_wgrad(const moe_experts_shape_t *shape, int32_t grad_w_fp32, const uint16_t *grad_out,
+                             const uint16_t *x, const int32_t *expert_offsets, void *grad_w, void *stream);
+
+/* Rows of bf16 to int8 or MXFP4: x [rows, features] -> codes, scales (layouts above).
+ *  row_type  MOE_ROWS_INT8: dyn = 127 / amax of the row, code = round-half-even(x * dyn) in [-127, 127],
+ *            scale 1 / dyn (moe_dispatch's dynamic mode without smooth scales; amax 0: codes 0, scale 0)
+ *            MOE_ROWS_MXFP4: per 32 elements s = floor(log2(amax)) - 2, at least -127; code = x / 2^s to the
+ *            nearest e2m1 value, ties to the even code, at most 6 in magnitude, the sign kept (also of zero);
+ *            amax 0: scale byte 0; a NaN or an infinity among the 32: scale byte 255, codes 0
+ *  shape, expert_offsets   both NULL: every row (the way to quantize weights: rows = num_experts * Nw);
+ *            else only the rows that belong to an expert of the layout (shape->rows = rows,
+ *            shape->in_features = features); out_features is not looked at
+ * features: at most 65536, a multiple of 16 (INT8) or 32 (MXFP4); 0 <= rows * features < 2^43. */
+int moe_quantize_rows(int32_t row_type, int64_t rows, int32_t features, const uint16_t *x, void *codes,
+                      void *scales, const moe_experts_shape_t *shape, const int32_t *expert_offsets, void *stream);
+
+/* Gradient of moe_combine.  With g = grad_out[t] and w = topk_weights[t, j]:
+ *   grad_expert_out[dst_row[t, j]] = bf16(w g)
+ *   grad_topk_weights[t, j] = <g, Moe_j(t)> (fp32; 0 for slots that add nothing and for masked tokens)
+ *   grad_ori_x[t] = bf16( sum over copy slots of w g + over constant slots of w alpha1[c] g )
+ *   grad_alpha1[c] = sum w g ori_x, grad_alpha2[c] = v[c] sum w g, grad_v[c] = alpha2[c] sum w g
+ *                    (sums over all slots with constant expert c, fp32)
+ * Shape, topk_idx, topk_weights, x_active_mask, dst_row, expert_out, ori_x and the const_* arrays as
+ * for moe_combine.  Every output may be NULL and is then not computed (not all of them); expert_out is
+ * needed only for grad_topk_weights.  Rows of grad_expert_out that dst_row does not name are left as
+ * they were; all other outputs are written whole.  grad_out and the bf16 arrays 16-byte aligned.  The
+ * gradient of bf16 moe_dispatch is moe_combine with unit weights.
+ *  out grad_expert_out [cap, H] bf16, grad_topk_weights [T, K] float32, grad_ori_x [T, H] bf16,
+ *      grad_alpha1, grad_alpha2, grad_v [Kc, H] float32 */
+int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, const uint16_t *expert_out,
+                     const int32_t *topk_idx, const float *topk_weights, const uint8_t *x_active_mask,
+                     const int32_t *dst_row, const uint16_t *ori_x, const uint16_t *const_alpha1,
+                     const uint16_t *const_alpha2, const uint16_t *const_v, uint16_t *grad_expert_out,
+                     float *grad_topk_weights, uint16_t *grad_ori_x, float *grad_alpha1, float *grad_alpha2,
+                     float *grad_v, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
