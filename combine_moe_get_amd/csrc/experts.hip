@@ -21,13 +21,45 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr uint32_t kOut = 0x80000000u;  // a byte offset past every buffer resource here: reads zero
 constexpr int kKB = 128;                // bytes of k per stage of a row operand
 constexpr int kKR = 64;                 // rows of k per stage of a column operand
+constexpr int kGroup = 8;               // tiles along m that are walked together
+constexpr uint32_t kOut = 0x80000000u;  // a byte offset past every buffer resource here: reads zero
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void *p, int64_t bytes) {
+// a raw buffer resource of `bytes` bytes (at most 2^31 - 1) at a wave-uniform address; the address has 48 bits
+__device__ __forceinline__ i32x4 resource(const void *p, int64_t bytes) {
+  const uint64_t u = (uint64_t)(uintptr_t)p;
   const int n = bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : (int)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc((void *)p, (short)0, n, 0x00020000);
+  return i32x4{__builtin_amdgcn_readfirstlane((int)(uint32_t)u), __builtin_amdgcn_readfirstlane((int)(u >> 32) & 0xffff),
+               __builtin_amdgcn_readfirstlane(n), 0x00020000};
+}
+
+// 64 lanes x 16 bytes from `off` + `soff` past the resource's base (behind its end: zeros) to LDS at `at` + `more` +
+// lane * 16; all but `off` wave-uniform.  Asm, because for its own loads into LDS the compiler waits before every
+// LDS read that it cannot prove disjoint, which here is each: stage_wait() waits instead.  No register is written.
+__device__ __forceinline__ void load_to_lds(i32x4 d, uint32_t off, uint32_t soff, uint32_t at, uint32_t more) {
+  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(d), "s"(soff),
+               "s"(at), "i"(more)
+               : "memory", "scc");
+}
+
+// until at most N of the wave's loads are under way and its LDS reads are done, then until every wave is there
+template <int N>
+__device__ __forceinline__ void stage_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// f(0), .., f(N - 1) with the index as a constant
+template <int I, int N, class F>
+__device__ __forceinline__ void static_for_from(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for_from<I + 1, N>(f);
+  }
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  static_for_from<0, N>(f);
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -35,28 +67,46 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+// g / (1 + exp(-g)); the exponential of a rounded argument and the reciprocal are good to about |g| + 4 steps of
+// fp32, far below the bf16 rounding that follows.  exp overflows to infinity: -0.
+__device__ __forceinline__ float silu(float g) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
+}
 
-// chunk permutation of the 16-byte chunks of a stage's rows, so that the lanes of one LDS read fall
-// on different banks: row operands are read 16 rows at a time, one chunk of each; column operands
-// four rows at a time, on the m side 32 bytes of each, on the n side four pieces of 8 bytes, 32 bytes apart
+// Permutation (an XOR of the index) of the 16-byte chunks of a stage's LDS rows, so that the lanes that one
+// cycle serves (128 bytes) fall on different banks.
+// Row operands: one chunk of each of 8 rows of 128 bytes.
 __device__ __forceinline__ int swz_row(int row) { return row & 7; }
+// Column operands: four rows of k (k & 3; on the m side 32 bytes of each, on the n side four pieces of 8 bytes,
+// 32 bytes apart).
 template <bool NSIDE>
 __device__ __forceinline__ int swz_col(int k) {
   return NSIDE ? (k & 1) | ((k & 2) << 2) : (k & 3) << 1;
 }
 
-template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN>
+// TY: row type; BM x BN: the tile (with the gate: BN / 2 columns of the result); WM x WN: its waves;
+// NST: stages in LDS; WIDE: MXFP4 scales of a row begin at multiples of four bytes
+template <int TY, int OP, bool GATED, int BM, int BN, int WM, int WN, int NST>
 struct Tile {
-  static constexpr int T = 64 * WM * WN;                         // threads
-  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // 16 x 16 results of a wave
-  static constexpr int CO = GATED ? BN / 2 : BN;                 // result columns
-  static constexpr bool MCOL = OP == OP_WGRAD, NCOL = OP != OP_FORWARD;
-  static constexpr int ABYTES = BM * kKB, BBYTES = BN * kKB;
-  static constexpr int AI = ABYTES / 1024 / (T / 64), BI = BBYTES / 1024 / (T / 64);  // loads of a wave per stage
+  static constexpr int W = WM * WN, T = 64 * W;               // waves, threads
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 results of a wave
+  static constexpr int CO = GATED ? BN / 2 : BN;              // result columns
+  static constexpr bool MCOL = OP == OP_WGRAD, NCOL = OP != OP_FORWARD, MX = TY == MOE_ROWS_MXFP4;
+  static constexpr int ABYTES = BM * kKB, BBYTES = BN * kKB, STAGE = ABYTES + BBYTES;
+  static constexpr int AI = ABYTES / 1024 / W, BI = BBYTES / 1024 / W;  // loads of a wave per stage
+  // MXFP4 scales: 16 bytes a row, enough for two stages; loads of a wave per two stages
+  static constexpr int SI = MX ? ((BM + BN) / 64 + W - 1) / W : 0, SBYTES = SI * W * 1024;
+  static constexpr int LDS = NST * STAGE + 2 * SBYTES;
   static constexpr int E16 = TY == MOE_ROWS_BF16 ? 8 : TY == MOE_ROWS_INT8 ? 16 : 32;  // elements in 16 bytes
   using Acc = typename std::conditional<TY == MOE_ROWS_INT8, i32x4, f32x4>::type;
-  static_assert(AI * 1024 * (T / 64) == ABYTES && BI * 1024 * (T / 64) == BBYTES, "whole loads");
+  static_assert(AI * 1024 * W == ABYTES && BI * 1024 * W == BBYTES, "whole loads");
+  // with the gate: halves of w that the rows of a wave's loads are of
+  static constexpr int HALVES = GATED && BI > FN ? 2 : 1;
+  static_assert(!GATED || FN % BI == 0 || BI == 2 * FN, "a load is of one half");
+  static_assert((!MCOL || BM >= 64) && (!NCOL || BN >= 128), "swz_col stays within a row");
+  static_assert(FN % 2 == 0, "the epilogue stores 8 columns, or 4 with the gate");
+  static_assert(!MX || BM % 64 == 0, "a load of scales is of one side");
+  static_assert(NST % 2 == 0 && (!MX || NST == 2), "scales are loaded one stage ahead of the first of their two");
 };
 
 // the n index (within the tile; for the gate: row of w relative to its half, and the half) of LDS row p
@@ -70,17 +120,21 @@ __device__ __forceinline__ int n_of(int p, int &half) {
   return b * 16 * F + (r / 4) * 4 * F + (f % F) * 4 + (r % 4);
 }
 
-template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM *WN) experts_kernel(ExpertsArgs a) {
-  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN>;
+#define LAMBDA __attribute__((always_inline))
+
+template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
+__global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) {
+  using C = Tile<TY, OP, GATED, BM, BN, WM, WN, NST>;
+  constexpr bool MX = C::MX;
   extern __shared__ __align__(1024) char lds[];
-  char *la = lds, *lb = lds + C::ABYTES;
-  int *first = (int *)(lds + C::ABYTES + C::BBYTES);  // [E + 1] tiles along m before each expert
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int *first = (int *)(lds + C::LDS);  // [E + 1] tiles along m before each expert
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int E = a.g.E;
   const int ntn = (a.N + C::CO - 1) / C::CO;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)lds;
 
+  const int lane = tid & 63;
   if (tid < 64) {  // tiles before each expert, 64 experts at a time
     int base = 0;
     const int most = (int)(a.g.rows / BM) + E;  // what ascending offsets give at most: keeps others in range
@@ -105,205 +159,392 @@ __global__ void __launch_bounds__(64 * WM *WN) experts_kernel(ExpertsArgs a) {
     if (lane == 0) first[E] = base;
   }
   __syncthreads();
-  const int64_t tiles = (int64_t)first[E] * ntn;
+  const uint32_t tiles = (uint32_t)first[E] * (uint32_t)ntn;  // fits: see launch_cfg
 
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int mg = (int)(tile / ntn);
-    int e = 0;  // the last expert whose tiles begin at or before mg and that has some
+  // Workgroups go round the 8 XCDs, each with an L2 of its own: XCD x takes the x-th eighth of the tiles, its
+  // workgroups neighbouring ones, so that those that run together share operands in that L2.
+  const uint32_t xcd = blockIdx.x & 7, per = (gridDim.x + 7 - xcd) >> 3;  // its workgroups
+  const uint32_t last = (uint32_t)((uint64_t)tiles * (xcd + 1) / 8);
+  uint32_t tile = (uint32_t)((uint64_t)tiles * xcd / 8) + (blockIdx.x >> 3);
+  if (tile >= last) return;
+
+  // byte strides of the operands' rows
+  const int64_t mrow = (int64_t)(OP == OP_WGRAD ? a.M : a.K) * 16 / C::E16;
+  const int64_t nrow = (int64_t)(OP == OP_FORWARD ? a.K : a.N) * 16 / C::E16;
+  const int nw = GATED ? 2 * a.N : a.N;  // forward: rows of an expert's weights
+  const int sw = a.K / 32;               // MXFP4: scales of a row
+
+  const int c16 = ((lane & 7) ^ swz_row(lane >> 3)) * 16;  // row operands: the lane's 16 of a load's 8 x 128 bytes
+
+  // ---- the tile whose stages are being loaded
+  int e, cnt, m0, n0, stages;
+  int64_t lo, klen;
+  const char *mbase, *nbase;
+  // A load of 1 KB takes 8 LDS rows of a row operand, or 512 / R rows of k of a column operand with rows of R
+  // columns.  Byte offsets of the lane's 16 bytes, the same in all stages:
+  uint32_t ao[C::AI], bo[C::BI], so[MX ? C::SI : 1];
+  const char *sbase[MX ? C::SI : 1];  // MXFP4 scales: of the operand of the wave's load, and their bytes
+  int sbytes[MX ? C::SI : 1];
+  i32x4 mres, nres[C::HALVES];  // row operands: over the tile's rows
+  auto enter = [&]() LAMBDA {
+    const uint32_t mg = tile / (uint32_t)ntn;
+    int x = 0;  // the last expert whose tiles begin at or before mg: it has some
     for (int step = 1024; step > 0; step >>= 1)
-      if (e + step < E && first[e + step] <= mg) e += step;
-    const int me = first[e + 1] - first[e];
-    const int rem = (int)(tile - (int64_t)first[e] * ntn);
-    const int nt = rem / me, mt = rem % me;
-    int64_t lo;
-    int cnt;
+      if (x + step < E && first[x + step] <= (int)mg) x += step;
+    e = __builtin_amdgcn_readfirstlane(x);
+    const int before = __builtin_amdgcn_readfirstlane(first[e]);
+    const int me = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
+    // the expert's tiles in groups of up to kGroup along m, in each along m first
+    const uint32_t rem = tile - (uint32_t)before * ntn, grp = rem / (uint32_t)(kGroup * ntn), in = rem - grp * kGroup * ntn;
+    const uint32_t gm = me - grp * kGroup < kGroup ? me - grp * kGroup : kGroup, nt = in / gm;
     expert_rows(a.g, e, lo, cnt);
+    m0 = (int)(grp * kGroup + in - nt * gm) * BM;
+    n0 = (int)nt * C::CO;
+    klen = OP == OP_WGRAD ? cnt : a.K;
+    mbase = (const char *)a.m + (OP == OP_WGRAD ? lo * mrow + (int64_t)m0 * 2 : (lo + m0) * mrow);
+    nbase = (const char *)a.n + (OP == OP_FORWARD ? ((int64_t)e * nw + n0) * nrow
+                                 : OP == OP_DGRAD ? (int64_t)e * a.K * nrow + (int64_t)n0 * 2
+                                                  : lo * nrow + (int64_t)n0 * 2);
+    stages = (int)(C::MCOL || C::NCOL ? (klen + kKR - 1) / kKR : (klen * 16 / C::E16 + kKB - 1) / kKB);
+#pragma unroll
+    for (int i = 0; i < C::AI; ++i) {
+      const int p = (wave * C::AI + i) * 64 + lane;
+      if (C::MCOL) {
+        const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<false>(k);
+        ao[i] = m0 + c * 8 < a.M ? (uint32_t)(k * (int)mrow + c * 16) : kOut;
+      } else {
+        ao[i] = m0 + p / 8 < cnt ? (uint32_t)(p / 8 * (int)mrow + c16) : kOut;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C::BI; ++i) {
+      const int p = (wave * C::BI + i) * 64 + lane;
+      if (C::NCOL) {
+        const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<true>(k);
+        bo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * (int)nrow + c * 16) : kOut;
+      } else {
+        int half;
+        const int n = n_of<C, GATED>(p / 8, half);
+        bo[i] = n0 + n < a.N ? (uint32_t)(n * (int)nrow + c16) : kOut;
+      }
+    }
+    if (!C::MCOL) mres = resource(mbase, 0x7fffffff);
+    if (!C::NCOL) {
+      const bool up = GATED && wave * C::BI * 8 % (16 * C::FN) >= 8 * C::FN;  // HALVES 1: the wave's half
+#pragma unroll
+      for (int h = 0; h < C::HALVES; ++h) nres[h] = resource(nbase + (up || h ? (int64_t)a.N * nrow : 0), 0x7fffffff);
+    }
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < C::SI; ++i) {  // LDS rows of scales: the m side's, then the n side's
+        const int p = (wave * C::SI + i) * 64 + lane;
+        const bool mside = (wave * C::SI + i) * 64 < BM;
+        sbase[i] = mside ? (const char *)a.ms + (lo + m0) * sw : (const char *)a.ns + ((int64_t)e * nw + n0) * sw;
+        const int64_t bytes = (int64_t)(mside ? cnt - m0 : nw - n0) * sw;
+        sbytes[i] = (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
+        if (p < BM) {
+          so[i] = m0 + p < cnt ? (uint32_t)(p * sw) : kOut;
+        } else if (p < BM + BN) {
+          int half;
+          const int n = n_of<C, GATED>(p - BM, half);
+          so[i] = n0 + n < a.N ? (uint32_t)((n + (GATED && half ? a.N : 0)) * sw) : kOut;
+        } else {
+          so[i] = kOut;
+        }
+      }
+    }
+  };
+  // load l (of AI + BI) of stage s into buffer b; past the last stage zeros, so that every stage counts the same
+  // loads
+  constexpr int LOADS = C::AI + C::BI;
+  const uint32_t mlds = lds0 + wave * C::AI * 1024, nlds = lds0 + NST * C::ABYTES + wave * C::BI * 1024;
+  auto issue = [&](int s, auto b_, auto l_) LAMBDA {
+    constexpr int b = decltype(b_)::value, l = decltype(l_)::value;
+    constexpr bool mside = l < C::AI;
+    constexpr int i = mside ? l : l - C::AI;
+    constexpr uint32_t more = (mside ? b * C::ABYTES : b * C::BBYTES) + i * 1024;
+    const int64_t row = mside ? mrow : nrow;
+    uint32_t o;
+    if constexpr (mside) o = ao[i];
+    else o = bo[i];
+    if constexpr (mside ? C::MCOL : C::NCOL) {  // rows of k past the last are outside of the resource
+      const int64_t k = (int64_t)s * kKR, bytes = (klen - k) * row - (int64_t)(mside ? m0 : n0) * 2;
+      load_to_lds(resource((mside ? mbase : nbase) + k * row, bytes), o, 0, mside ? mlds : nlds, more);
+    } else {  // a piece that begins behind its row's end is not read
+      load_to_lds(mside ? mres : nres[C::HALVES == 2 ? i / C::FN : 0], c16 < (int)row - s * kKB ? o : kOut, s * kKB,
+                  mside ? mlds : nlds, more);
+    }
+  };
+  // the scales of stages 2 t and 2 t + 1, 16 bytes a row (the last piece may run on into the next row's: see
+  // scales), into the other of their two buffers
+  int sbuf = 1;
+  auto issue_scales = [&](int t) LAMBDA {
+#pragma unroll
+    for (int i = 0; i < C::SI; ++i) {
+      const uint32_t at = lds0 + NST * C::STAGE + (sbuf ^ 1) * C::SBYTES + (wave * C::SI + i) * 1024;
+      if constexpr (WIDE) {
+        load_to_lds(resource(sbase[i] + t * 16, t * 16 < sw ? sbytes[i] - t * 16 : 0), so[i], 0, at, 0);
+      } else {  // a byte at a time through registers; zeros behind the rows' end
+        u32x4 v = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+          if (so[i] != kOut && t * 16 + q < sw) v[q / 4] |= (uint32_t)(uint8_t)sbase[i][(int64_t)so[i] + t * 16 + q] << (q % 4 * 8);
+        *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(at + lane * 16) = v;
+      }
+    }
+  };
 
-    const int m0 = mt * BM, n0 = nt * C::CO;
-    const int mlim = OP == OP_WGRAD ? a.M : cnt;  // rows of the result
-    const int64_t klen = OP == OP_WGRAD ? cnt : a.K;
-    // byte strides of the operands' rows
-    const int64_t mrow = (int64_t)(OP == OP_WGRAD ? a.M : a.K) * 16 / C::E16;
-    const int64_t nrow = (int64_t)(OP == OP_FORWARD ? a.K : a.N) * 16 / C::E16;
-    const int nw = GATED ? 2 * a.N : a.N;  // forward: rows of an expert's weights
-    const char *mbase = (const char *)a.m + (OP == OP_WGRAD ? lo * mrow + (int64_t)m0 * 2 : (lo + m0) * mrow);
-    const char *nbase = (const char *)a.n + (OP == OP_FORWARD ? ((int64_t)e * nw + n0) * nrow
-                                             : OP == OP_DGRAD ? (int64_t)e * a.K * nrow + (int64_t)n0 * 2
-                                                              : lo * nrow + (int64_t)n0 * 2);
+  // ---- the lane's part of 16 rows and 64 bytes of k (one matrix instruction deep) of a stage in buffer b:
+  // lane group g has the 16-byte piece 2 g + ks of the stage's 8
+  const int g = lane >> 4, r16 = lane & 15;
+  // LDS holds the m side's NST buffers, then the n side's (so that within one an offset fits the instruction), then
+  // the scales.  Addresses in buffer 0; the rest of a piece's address is constant (an XOR with a constant for columns).
+  // The empty asm statement keeps them in registers as they are.
+  const int mfirst = wm * (BM / WM), nfirst = wn * (BN / WN), kt = g * 16 + (r16 >> 2);
+  uint32_t ma[2], na[2];
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    // rows: of piece ks; swz_row is the same in every sixteenth row
+    const uint32_t piece = r16 * kKB + (((g * 2 + ks) ^ swz_row(r16)) << 4);
+    ma[ks] = lds0 + mfirst * kKB + piece;
+    na[ks] = lds0 + NST * C::ABYTES + nfirst * kKB + piece;
+  }
+  // columns: swz_col looks only at bits of k that ks and u leave alone
+  if (C::MCOL) ma[0] = lds0 + kt * BM * 2 + ((((mfirst + (lane & 3) * 4) >> 3) ^ swz_col<false>(kt)) << 4) + (lane & 1) * 8;
+  if (C::NCOL) na[0] = lds0 + NST * C::ABYTES + kt * BN * 2 + (((nfirst + (lane & 3) * 4 * C::FN) >> 3 ^ swz_col<true>(kt)) << 4);
+  uint32_t sm = lds0 + NST * C::STAGE + (mfirst + r16) * 16 + g * 2, sn = sm + (BM + nfirst - mfirst) * 16;  // scales
+  asm volatile("" : "+v"(ma[0]), "+v"(ma[1]), "+v"(na[0]), "+v"(na[1]), "+v"(sm), "+v"(sn));
+  auto column = [&](uint32_t at, int R) LAMBDA {  // 8 rows of k, four columns of each
+    s16x4 h[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(uintptr_t)(at + u * 4 * R * 2));
+    return __builtin_bit_cast(i32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read_m = [&](int b, int i, int ks) LAMBDA -> i32x4 {
+    if (C::MCOL) return column((ma[0] ^ (i << 5)) + b * C::ABYTES + ks * 8 * BM * 2, BM);
+    return *(__attribute__((address_space(3))) const i32x4 *)(uintptr_t)(ma[ks] + b * C::ABYTES + i * 16 * kKB);
+  };
+  auto read_n = [&](int b, int j, int ks) LAMBDA -> i32x4 {
+    if (C::NCOL) return column((na[0] ^ ((j >> 1) << 4)) + (j & 1) * 8 + b * C::BBYTES + ks * 8 * BN * 2, BN);
+    return *(__attribute__((address_space(3))) const i32x4 *)(uintptr_t)(na[ks] + b * C::BBYTES + j * 16 * kKB);
+  };
+  // MXFP4: the scale bytes of the lane's two pieces of stage s (even: b = 0), of two rows in one register
+  constexpr int SM = MX ? (C::FM + 1) / 2 : 1, SN = MX ? (C::FN + 1) / 2 : 1;
+  uint32_t sa[SM], sb[SN];
+  auto scale_pair = [&](uint32_t p, int s, int b, int i, int n) LAMBDA -> uint32_t {
+    typedef __attribute__((address_space(3))) const uint16_t *lds_u16;
+    const uint32_t at = p + sbuf * C::SBYTES + b * 8 + i * 512;
+    uint32_t v = *(lds_u16)(uintptr_t)at;
+    if (2 * i + 1 < n) v |= (uint32_t) * (lds_u16)(uintptr_t)(at + 256) << 16;
+    // blocks behind the rows' end: not the next rows' scales, which may be NaN (sw is a multiple of 4)
+    return !WIDE || s * 8 + g * 2 < sw ? v : 0;
+  };
 
-    typename C::Acc acc[C::FM][C::FN];
+  typename C::Acc acc[C::FM][C::FN];
+  i32x4 fa[2][C::FM], fb[2][C::FN];  // pieces of this step of 64 bytes of k, and of the next
+  auto multiply = [&](auto ks_, auto i_) LAMBDA {  // row i of the wave's results
+    constexpr int ks = decltype(ks_)::value, i = decltype(i_)::value;
+    static_for<C::FN>([&](auto j_) LAMBDA {
+      constexpr int j = decltype(j_)::value;
+      if constexpr (TY == MOE_ROWS_BF16) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[ks][j]),
+                                                            __builtin_bit_cast(bf16x8, fa[ks][i]), acc[i][j], 0, 0, 0);
+      } else if constexpr (TY == MOE_ROWS_INT8) {
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[ks][j], fa[ks][i], acc[i][j], 0, 0, 0);
+      } else {
+        const i32x4 n4 = fb[ks][j], m4 = fa[ks][i];
+        const i32x8 vb = {n4[0], n4[1], n4[2], n4[3], 0, 0, 0, 0};
+        const i32x8 va = {m4[0], m4[1], m4[2], m4[3], 0, 0, 0, 0};
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc[i][j], 4, 4, (j & 1) * 2 + ks, sb[j / 2],
+                                                                     (i & 1) * 2 + ks, sa[i / 2]);
+      }
+    });
+  };
+
+  // ---- a stage, in buffer b of the ring.  The products of one step of 64 bytes of k run while the next step's
+  // operands come from LDS.  Before those are the next stage's, every wave has read this stage, so its buffer
+  // takes the loads of stage `ahead`, and the next stage's loads have to be there.  after: the next stage
+  auto stage = [&](auto b_, int after, int ahead) LAMBDA {
+    constexpr int b = decltype(b_)::value, bn = (b + 1) % NST;
+    static_for<2>([&](auto ks_) LAMBDA {
+      constexpr int ks = decltype(ks_)::value;
+      if constexpr (ks == 1) {
+        stage_wait<(NST - 2) * LOADS>();
+        if constexpr (MX) {
+          if (b == 1) sbuf ^= 1;
+          if (b == 0) issue_scales(ahead / 2);
+        }
+      }
+      static_for<C::FM>([&](auto i_) LAMBDA {
+        constexpr int i = decltype(i_)::value;
+        multiply(ks_, i_);
+        if constexpr (ks == 1) {
+          static_for_from<i * LOADS / C::FM, (i + 1) * LOADS / C::FM>([&](auto l_) LAMBDA { issue(ahead, b_, l_); });
+        }
+#pragma unroll
+        for (int j = i * C::FN / C::FM; j < (i + 1) * C::FN / C::FM; ++j) fb[ks ^ 1][j] = read_n(ks == 1 ? bn : b, j, ks ^ 1);
+        fa[ks ^ 1][i] = read_m(ks == 1 ? bn : b, i, ks ^ 1);
+        if constexpr (MX && ks == 1) {  // the next stage's scales, where this one's are done with
+          if constexpr (i % 2 == 1 || i == C::FM - 1) sa[i / 2] = scale_pair(sm, after, bn, i / 2, C::FM);
+          if constexpr (i == C::FM - 1) {
+#pragma unroll
+            for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, after, bn, j, C::FN);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+  };
+
+  auto fill = [&]() LAMBDA {
+    sbuf = 1;
+    if constexpr (MX) issue_scales(0);
+    sbuf = 0;
+    static_for<NST>([&](auto b_) LAMBDA { static_for<LOADS>([&](auto l_) LAMBDA { issue(decltype(b_)::value, b_, l_); }); });
+  };
+  auto begin = [&]() LAMBDA {
+    stage_wait<(NST - 1) * LOADS>();
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < SM; ++i) sa[i] = scale_pair(sm, 0, 0, i, C::FM);
+#pragma unroll
+      for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, 0, 0, j, C::FN);
+    }
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) fb[0][j] = read_n(0, j, 0);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) fa[0][i] = read_m(0, i, 0);
+  };
+
+  enter();
+  fill();
+  if constexpr (RING) begin();
+  for (;;) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = typename C::Acc{0, 0, 0, 0};
-
-    const int stages = (int)(C::MCOL || C::NCOL ? (klen + kKR - 1) / kKR : (klen * 16 / C::E16 + kKB - 1) / kKB);
-    for (int s = 0; s < stages; ++s) {
-      // ---- the stage's operands to LDS, 1 KB a load: lane l's 16 bytes land at l * 16
-      const char *mp = mbase + (C::MCOL ? (int64_t)s * kKR * mrow : (int64_t)s * kKB);
-      const char *np = nbase + (C::NCOL ? (int64_t)s * kKR * nrow : (int64_t)s * kKB);
-      const __amdgpu_buffer_rsrc_t mr = resource(mp, 0x7fffffff);
-#pragma unroll
-      for (int i = 0; i < C::AI; ++i) {
-        const int p = (wave * C::AI + i) * 64 + lane;
-        uint32_t off;
-        if (C::MCOL) {
-          const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<false>(k);
-          off = (int64_t)s * kKR + k < klen && m0 + c * 8 < a.M ? (uint32_t)(k * mrow + c * 16) : kOut;
-        } else {
-          const int r = p / 8, c = (p % 8) ^ swz_row(r);
-          off = m0 + r < cnt && (int64_t)s * kKB + c * 16 < mrow ? (uint32_t)(r * mrow + c * 16) : kOut;
-        }
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(mr, (lds_char *)(la + (wave * C::AI + i) * 1024), 16, off, 0, 0, 0);
+    if constexpr (!RING) begin();
+    // whole turns of the buffers, so that each tile begins at the first: up to NST - 1 stages of zeros more
+    const int turns = stages > NST ? (stages + NST - 1) / NST : 1, full = RING ? turns - 1 : turns;
+    for (int s0 = 0; s0 < full * NST; s0 += NST)
+      static_for<NST>([&](auto b_) LAMBDA { stage(b_, s0 + decltype(b_)::value + 1, s0 + decltype(b_)::value + NST); });
+    const int m1 = m0, n1 = n0, e1 = e, mlim = OP == OP_WGRAD ? a.M : cnt;  // mlim: rows of the result
+    const int64_t lo1 = lo;
+    tile += per;
+    if constexpr (RING) {  // the last turn loads the next tile's first stages
+      if (tile < last) enter();  // else this one's again, for nothing
+      static_for<NST>([&](auto b_) LAMBDA {
+        constexpr int b = decltype(b_)::value;
+        stage(b_, b + 1 < NST ? (turns - 1) * NST + b + 1 : 0, b);
+      });
+    } else {  // the next tile's first loads go out before this one's results
+      stage_wait<0>();
+      if (tile < last) {
+        enter();
+        fill();
       }
-#pragma unroll
-      for (int i = 0; i < C::BI; ++i) {
-        const int p = (wave * C::BI + i) * 64 + lane;
-        uint32_t off;
-        if (C::NCOL) {
-          const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<true>(k);
-          off = (int64_t)s * kKR + k < klen && n0 + c * 8 < a.N ? (uint32_t)(k * nrow + c * 16) : kOut;
-        } else {
-          const int r = p / 8, c = (p % 8) ^ swz_row(r);
-          int half;
-          const int n = n_of<C, GATED>(r, half);
-          off = n0 + n < a.N && (int64_t)s * kKB + c * 16 < nrow ? (uint32_t)(n * nrow + c * 16) : kOut;
-        }
-        // the eight rows of one load are of one half
-        const bool up = GATED && ((wave * C::BI + i) * 8 % (16 * C::FN)) / 16 >= C::FN / 2;
-        const __amdgpu_buffer_rsrc_t nr = resource(np + (up ? (int64_t)a.N * nrow : 0), 0x7fffffff);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(nr, (lds_char *)(lb + (wave * C::BI + i) * 1024), 16, off, 0, 0, 0);
-      }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();
-
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {  // 64 bytes of k: one matrix instruction deep
-        i32x4 fa[C::FM], fb[C::FN];
-        const int g = lane >> 4, r16 = lane & 15;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-          if (C::MCOL) {
-            const int m = wm * (BM / WM) + i * 16 + (lane & 3) * 4;
-            s16x4 h[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int k = ks * 32 + g * 8 + u * 4 + (r16 >> 2);
-              h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4 *)(la + k * BM * 2 + (((m >> 3) ^ swz_col<false>(k)) << 4) + (m & 7) * 2));
-            }
-            fa[i] = __builtin_bit_cast(i32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-          } else {
-            const int r = wm * (BM / WM) + i * 16 + r16;
-            fa[i] = *(const i32x4 *)(la + r * kKB + (((ks * 4 + g) ^ swz_row(r)) << 4));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          if (C::NCOL) {
-            const int n = wn * (BN / WN) + (lane & 3) * 4 * C::FN + j * 4;
-            s16x4 h[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int k = ks * 32 + g * 8 + u * 4 + (r16 >> 2);
-              h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4 *)(lb + k * BN * 2 + (((n >> 3) ^ swz_col<true>(k)) << 4) + (n & 7) * 2));
-            }
-            fb[j] = __builtin_bit_cast(i32x4, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
-          } else {
-            const int r = wn * (BN / WN) + j * 16 + r16;
-            fb[j] = *(const i32x4 *)(lb + r * kKB + (((ks * 4 + g) ^ swz_row(r)) << 4));
-          }
-        }
-        int sa[C::FM], sb[C::FN];
-        if constexpr (TY == MOE_ROWS_MXFP4) {  // the lane's block of 32: one scale byte a row
-          const int sw = a.K / 32, blk = s * 8 + ks * 4 + g;
-#pragma unroll
-          for (int i = 0; i < C::FM; ++i) {
-            const int m = m0 + wm * (BM / WM) + i * 16 + r16;
-            sa[i] = m < cnt && blk < sw ? ((const uint8_t *)a.ms)[(lo + m) * sw + blk] : 0;
-          }
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j) {
-            int half;
-            const int n = n0 + n_of<C, GATED>(wn * (BN / WN) + j * 16 + r16, half);
-            sb[j] = n < a.N && blk < sw
-                        ? ((const uint8_t *)a.ns)[((int64_t)e * nw + n + (GATED && half ? a.N : 0)) * sw + blk]
-                        : 0;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j) {
-            if constexpr (TY == MOE_ROWS_BF16) {
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[j]),
-                                                                  __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0, 0, 0);
-            } else if constexpr (TY == MOE_ROWS_INT8) {
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
-            } else {
-              const i32x8 vb = {fb[j][0], fb[j][1], fb[j][2], fb[j][3], 0, 0, 0, 0};
-              const i32x8 va = {fa[i][0], fa[i][1], fa[i][2], fa[i][3], 0, 0, 0, 0};
-              acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, acc[i][j], 4, 4, 0, sb[j], 0, sa[i]);
-            }
-          }
-      }
-      __syncthreads();
     }
+    // the products are finished here, not moved behind the branches below
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(acc[i][j]));
 
-    // ---- epilogue: lane (g, r16) holds, of result row i * 16 + r16, 4 FN consecutive columns
+    // ---- results: lane (g, r16) holds, of row i * 16 + r16, 4 FN consecutive columns
     constexpr int F = GATED ? C::FN / 2 : C::FN;
-    const int g = lane >> 4, r16 = lane & 15;
-    const int nl = n0 + wn * 16 * F + g * 4 * F;
+    const int l = lane, nl = n1 + wn * 16 * F + (l >> 4) * 4 * F;
+    float cs[TY == MOE_ROWS_INT8 ? 4 * C::FN : 1];  // the columns' scales
+    if constexpr (TY == MOE_ROWS_INT8) {
+#pragma unroll
+      for (int q = 0; q < 4 * C::FN; ++q) {
+        const int n = nl + q % (4 * F);
+        cs[q] = a.ns && n < a.N ? ((const float *)a.ns)[(int64_t)e1 * nw + n + (q >= 4 * F ? a.N : 0)] : 1.0f;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      const int m = m0 + wm * (BM / WM) + i * 16 + r16;
+      const int m = m1 + mfirst + i * 16 + (l & 15);
       if (m >= mlim) continue;
-      const float rs = TY == MOE_ROWS_INT8 && a.ms ? ((const float *)a.ms)[lo + m] : 1.0f;
+      const float rs = TY == MOE_ROWS_INT8 && a.ms ? ((const float *)a.ms)[lo1 + m] : 1.0f;
       float v[4 * C::FN];
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float y = (float)acc[i][j][q];
-          if constexpr (TY == MOE_ROWS_INT8) {
-            const int n = nl + (j % F) * 4 + q;
-            if (a.ns && n < a.N) y *= ((const float *)a.ns)[(int64_t)e * nw + n + (j >= F ? a.N : 0)];
-            y *= rs;
-          }
-          v[j * 4 + q] = y;
-        }
+      for (int q = 0; q < 4 * C::FN; ++q) {
+        v[q] = (float)acc[i][q / 4][q % 4];
+        if constexpr (TY == MOE_ROWS_INT8) v[q] = v[q] * cs[q] * rs;
+      }
       if constexpr (GATED) {
 #pragma unroll
         for (int q = 0; q < 4 * F; ++q) v[q] = silu(v[q]) * v[4 * F + q];
       }
-      const int64_t row = (OP == OP_WGRAD ? (int64_t)e * a.M : lo) + m;
+      const int64_t row = (OP == OP_WGRAD ? (int64_t)e1 * a.M : lo1) + m;
+      if constexpr (F == 1) {  // four columns
+        static_assert(!F32, "");
+        if (nl < a.N) *(u32x2 *)((uint16_t *)a.out + row * a.N + nl) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4 * F; q += 8) {
-        if (nl + q >= a.N) continue;  // N is a multiple of 8
-        if constexpr (F32) {
-          f32x4 *o = (f32x4 *)((float *)a.out + row * a.N + nl + q);
-          o[0] = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
-          o[1] = f32x4{v[q + 4], v[q + 5], v[q + 6], v[q + 7]};
-        } else {
-          *(u32x4 *)((uint16_t *)a.out + row * a.N + nl + q) =
-              u32x4{pack2(v[q], v[q + 1]), pack2(v[q + 2], v[q + 3]), pack2(v[q + 4], v[q + 5]), pack2(v[q + 6], v[q + 7])};
+        for (int q = 0; q < 4 * F; q += 8) {
+          if (nl + q >= a.N) continue;  // N is a multiple of 8
+          if constexpr (F32) {
+            f32x4 *o = (f32x4 *)((float *)a.out + row * a.N + nl + q);
+            o[0] = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
+            o[1] = f32x4{v[q + 4], v[q + 5], v[q + 6], v[q + 7]};
+          } else {
+            *(u32x4 *)((uint16_t *)a.out + row * a.N + nl + q) =
+                u32x4{pack2(v[q], v[q + 1]), pack2(v[q + 2], v[q + 3]), pack2(v[q + 4], v[q + 5]), pack2(v[q + 6], v[q + 7])};
+          }
         }
       }
     }
+    if (tile >= last) break;
   }
+  stage_wait<0>();  // nothing is under way into LDS when the workgroup gives it back
 }
+#undef LAMBDA
 
-template <int TY, int OP, bool GATED, bool F32>
-static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
-  constexpr int BM = 128, BN = 128, WM = 2, WN = 2;
-  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN>;
+template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
+static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
+  using C = Tile<TY, OP, GATED, BM, BN, WM, WN, NST>;
+  // at most (2^27 / 64 + 2^11) * 2^10 or 2^21 * 2^10 tiles: below 2^32
   const int64_t mt = OP == OP_WGRAD ? (int64_t)a.g.E * ((a.M + BM - 1) / BM) : a.g.rows / BM + a.g.E;
   const int64_t tiles = mt * ((a.N + C::CO - 1) / C::CO);
-  const size_t lds = C::ABYTES + C::BBYTES + (size_t)(a.g.E + 1) * 4;
-  const unsigned grid = (unsigned)(tiles < 1024 ? tiles : 1024);
-  hipLaunchKernelGGL((experts_kernel<TY, OP, GATED, F32, BM, BN, WM, WN>), dim3(grid), dim3(C::T), lds, st, a);
+  const size_t lds = C::LDS + (size_t)(a.g.E + 1) * 4;
+  const int64_t resident = 256 * (160 * 1024 / lds > 8 / C::W ? 8 / C::W : 160 * 1024 / lds);
+  const unsigned grid = (unsigned)(tiles < resident ? (tiles + 7) / 8 * 8 : resident);
+  auto k = experts_kernel<TY, OP, GATED, F32, BM, BN, WM, WN, NST, RING, WIDE>;
+  hipLaunchKernelGGL(k, dim3(grid), dim3(C::T), lds, st, a);
   return hipGetLastError();
+}
+// The tile.  Figures: us on one MI355X, every operand from HBM; `mean` is rows per expert.
+//  16 x 64, 2 waves    forward, mean <= 16: weights streamed once, four or so workgroups a CU.  8 experts with a row,
+//                      4096 -> 2 x 1024 bf16: 22 against 28 (128 x 128)
+//  64 x 128, 4 waves   mean <= 64
+//  128 x 128, 4 waves, four stages     at most a tile a CU: depth counts.  8 x 128 rows, 7168 -> 2 x 2048 int8: 55
+//                      against 70 with two stages (two workgroups a CU), 91 with 256 x 256
+//  256 x 256, 8 waves  tiles for most CUs and long sums: 16 x 2048 rows, 4096 -> 4096: 881 against 1175 (128 x 128)
+//  128 x 128, two stages, two workgroups a CU     the rest
+// MXFP4 has two stages always (see Tile).
+template <int TY, int OP, bool GATED, bool F32>
+static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
+  constexpr bool MX = TY == MOE_ROWS_MXFP4;
+  constexpr int DEEP = MX ? 2 : 4;
+  const int64_t mean = (a.g.rows + a.g.E - 1) / a.g.E, m = OP == OP_WGRAD ? a.M : mean;
+  auto tiles = [&](int bm, int bn) {
+    if (GATED) bn /= 2;
+    return a.g.E * ((m + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+  };
+  if constexpr (MX) {
+    if (a.K % 128 != 0) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, false>(a, st);
+  }
+  if constexpr (OP == OP_FORWARD && !MX) {
+    if (mean <= 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);
+  }
+  if (m <= 64) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, DEEP, true, true>(a, st);
+  if (!MX && tiles(128, 128) <= 256) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, DEEP, true, true>(a, st);
+  if (tiles(256, 256) >= 200 && mean >= (OP == OP_WGRAD ? 512 : 128))
+    return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, true>(a, st);
+  return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
 }
 
 hipError_t launch_experts(const ExpertsArgs &a, int op, int row_type, int act, bool out_fp32, hipStream_t st) {

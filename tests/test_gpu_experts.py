@@ -88,7 +88,7 @@ def test_int8_largest_sum_is_exact():
 
 
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
-@pytest.mark.parametrize("K,N", [(32, 8), (96, 24), (288, 136), (1056, 264), (2048, 136)])
+@pytest.mark.parametrize("K,N", [(32, 8), (96, 24), (128, 72), (288, 136), (640, 264), (1056, 264), (2048, 136)])
 @pytest.mark.parametrize("counts", RAGGED, ids=_counts_id)
 def test_mxfp4(counts, K, N, gated):
     print(f"[experts mxfp4] {counts} K={K} N={N} gated={gated}", flush=True)
@@ -231,6 +231,62 @@ def test_larger(counts, K, N):
     mg.experts_matmul(rows.shape(K, N), X.poison(x, rows.used).to(X.DEV), w.to(X.DEV), rows.dev_off(), out=out)
     X.check(out, ref, tol, rows.used, "bf16")
     _backward(rows, K, N, r, torch.bfloat16)
+
+
+# counts, N: several tiles for each workgroup that is resident, for every tile shape that the sizes select
+SHAPES = {
+    "16 rows": ([8, 0, 15, 3] * 24, 1544),
+    "64 rows": ([40, 64, 65, 0] * 24, 1544),
+    "128 rows": ([100, 129, 1, 130] * 24, 1544),
+    "few tiles": ([129, 260, 7, 300], 1032),
+    "256 rows": ([700, 513, 256, 1, 999, 0, 1500, 300] * 2, 3080),
+}
+
+
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("row_type", ["bf16", "int8", "mxfp4"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_tile_shapes(name, row_type, gated):
+    counts, N = SHAPES[name]
+    K = 416 if row_type == "bf16" else 400 if row_type == "int8" else 384
+    N = N // 2 // 8 * 8 if gated else N
+    print(f"[experts shapes] {name} {row_type} gated={gated} N={N} K={K}", flush=True)
+    r = np.random.default_rng([11, N, K])
+    rows = X.Rows(counts)
+    nw = N * (2 if gated else 1)
+    t = torch.from_numpy
+    xs = ws = None
+    if row_type == "bf16":
+        x, w = X.bf16(r, rows.rows, K), X.bf16(r, rows.E, nw, K, scale=K ** -0.5)
+        x64, w64 = X.f64(x), X.f64(w)
+    elif row_type == "int8":
+        x, w = (t(r.integers(-127, 128, s, dtype=np.int8)) for s in ((rows.rows, K), (rows.E, nw, K)))
+        xs, ws = (t(r.uniform(0.5, 2, s).astype(np.float32) / 70) for s in ((rows.rows,), (rows.E, nw)))
+        ws /= K ** 0.5
+        x64, w64 = X.f64(x) * X.f64(xs)[:, None], X.f64(w) * X.f64(ws)[..., None]
+    else:
+        x, w = (t(r.integers(0, 256, s, dtype=np.uint8)) for s in ((rows.rows, K // 2), (rows.E, nw, K // 2)))
+        xs = t(r.integers(122, 129, (rows.rows, K // 32), dtype=np.uint8))
+        ws = t(r.integers(116, 123, (rows.E, nw, K // 32), dtype=np.uint8))
+        x64, w64 = X.unpack_mx(x.numpy(), xs.numpy()), X.unpack_mx(w.numpy(), ws.numpy())
+    ref, tol = X.product(rows, x64, w64, gated)
+    d = lambda a: None if a is None else a.to(X.DEV)  # noqa: E731
+    xd, wd, xsd, wsd = d(X.poison(x, rows.used)), d(w), d(xs), d(ws)
+    outs = []
+    for _ in range(2):
+        out = X.canary(rows.rows, N)
+        mg.experts_matmul(rows.shape(K, N), xd, wd, rows.dev_off(), xsd, wsd,
+                          mg.ACT_SWIGLU if gated else mg.ACT_NONE, out)
+        outs.append(out)
+    X.check(outs[0], ref, tol, rows.used, name)
+    assert torch.equal(outs[0], outs[1]), "the same call twice"
+
+
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_tile_shapes_of_gradients(name):
+    counts, N = SHAPES[name]
+    print(f"[experts shapes] {name} gradients", flush=True)
+    _backward(X.Rows(counts), 416 if N < 2000 else 1040, N // 2 // 8 * 8, np.random.default_rng(12), torch.bfloat16)
 
 
 def test_many_experts():
