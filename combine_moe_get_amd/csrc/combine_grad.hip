@@ -30,54 +30,81 @@ __device__ __forceinline__ void unpack8g(const u32x4 &v, float *f) {
 
 enum : int { G_NONE = 0, G_ROUTED = 1, G_COPY = 2, G_CONST = 3 };
 
-template <int KMAX, int THREADS>
-__global__ void __launch_bounds__(THREADS) combine_grad_kernel(CombineGradArgs a) {
+// One workgroup a token, a thread U chunks of 8 elements; threads past the row's end only take part in the sums.
+// The slots' kinds, rows and weights are wave-uniform; every row of a chunk is requested before the first is used.
+// SPECIAL: copy and constant experts can occur.
+template <int KMAX, int U, bool SPECIAL>
+__global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;
-  __shared__ float part[THREADS / 64][KMAX];
+  __shared__ float part[16][KMAX];
   const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int H = c.H, K = c.K, nch = H >> 3;
   const bool live = !c.mask || c.mask[t];
 
+  int id = -1, r = -1;
+  float wt = 0.0f;
+  if (lane < K) {
+    id = c.topk_idx[(size_t)t * K + lane];
+    wt = c.w[(size_t)t * K + lane];
+    r = c.dst_row[(size_t)t * K + lane];
+  }
+  u32x4 gv[U], xv[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int ch = tid + u * blockDim.x;
+    gv[u] = xv[u] = u32x4{0u, 0u, 0u, 0u};
+    if (ch < nch) {
+      gv[u] = ((const u32x4 *)(a.go + (size_t)t * H))[ch];
+      if (SPECIAL) xv[u] = ((const u32x4 *)(c.ori_x + (size_t)t * H))[ch];
+    }
+  }
+  int k = G_NONE;
+  if (live && lane < K) {
+    const int zc = c.E + c.Z;
+    if (id >= 0 && id < c.E) {
+      k = r >= 0 ? G_ROUTED : G_NONE;
+    } else if (SPECIAL && id >= zc && id < zc + c.C) {
+      k = G_COPY;
+    } else if (SPECIAL && id >= zc + c.C && id < zc + c.C + c.Kc) {
+      k = G_CONST;
+      r = id - zc - c.C;
+    }
+  }
   int kind[KMAX], row[KMAX];  // row: of expert_out, or of the constant experts' vectors
   float w[KMAX], dot[KMAX];
 #pragma unroll
   for (int j = 0; j < KMAX; ++j) {
-    kind[j] = G_NONE;
-    row[j] = 0;
-    w[j] = dot[j] = 0.0f;
-    if (j < K && live) {
-      const int id = c.topk_idx[(size_t)t * K + j];
-      w[j] = c.w[(size_t)t * K + j];
-      const int zc = c.E + c.Z;
-      if (id >= 0 && id < c.E) {
-        row[j] = c.dst_row[(size_t)t * K + j];
-        kind[j] = row[j] >= 0 ? G_ROUTED : G_NONE;
-      } else if (id >= zc && id < zc + c.C) {
-        kind[j] = G_COPY;
-      } else if (id >= zc + c.C && id < zc + c.C + c.Kc) {
-        kind[j] = G_CONST;
-        row[j] = id - zc - c.C;
-      }
-    }
+    kind[j] = readlane(k, j);
+    row[j] = readlane(r, j);
+    w[j] = readlane_f(wt, j);
+    dot[j] = 0.0f;
   }
-  for (int ch = tid; ch < nch; ch += THREADS) {
-    float g[8], x[8], gx[8];
-    unpack8g(((const u32x4 *)(a.go + (size_t)t * H))[ch], g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gx[e] = x[e] = 0.0f;
-    if (c.ori_x) unpack8g(((const u32x4 *)(c.ori_x + (size_t)t * H))[ch], x);
+  for (int u = 0; u < U; ++u) {
+    const int ch = tid + u * blockDim.x;
+    const bool in = ch < nch;
+    u32x4 yv[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      yv[j] = u32x4{0u, 0u, 0u, 0u};
+      if (kind[j] == G_ROUTED && a.gw && in) yv[j] = __builtin_nontemporal_load((const u32x4 *)c.y + (size_t)row[j] * nch + ch);
+    }
+    float g[8], x[8], gx[8];
+    unpack8g(gv[u], g);
+    unpack8g(xv[u], x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) gx[e] = 0.0f;
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
       if (kind[j] == G_NONE) continue;
       float y[8];
-      if (kind[j] == G_ROUTED) {
-        const size_t at = (size_t)row[j] * nch + ch;
-        if (a.gw) unpack8g(((const u32x4 *)c.y)[at], y);
-        if (a.gy) {
+      if (!SPECIAL || kind[j] == G_ROUTED) {
+        unpack8g(yv[j], y);
+        if (a.gy && in) {
           u32x4 o;
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[e] = pack2g(w[j] * g[2 * e], w[j] * g[2 * e + 1]);
-          ((u32x4 *)a.gy)[at] = o;
+          __builtin_nontemporal_store(o, (u32x4 *)a.gy + (size_t)row[j] * nch + ch);
         }
       } else if (kind[j] == G_COPY) {
 #pragma unroll
@@ -87,7 +114,7 @@ __global__ void __launch_bounds__(THREADS) combine_grad_kernel(CombineGradArgs a
         }
       } else {
         float a1[8], a2[8], v[8];
-        const size_t at = (size_t)row[j] * nch + ch;
+        const size_t at = (size_t)row[j] * nch + (in ? ch : 0);  // threads past the end: g = 0
         unpack8g(((const u32x4 *)c.a1)[at], a1);
         unpack8g(((const u32x4 *)c.a2)[at], a2);
         unpack8g(((const u32x4 *)c.cv)[at], v);
@@ -97,17 +124,20 @@ __global__ void __launch_bounds__(THREADS) combine_grad_kernel(CombineGradArgs a
           gx[e] = __builtin_fmaf(w[j] * a1[e], g[e], gx[e]);
         }
       }
-      if (a.gw) {
+      if (a.gw && in) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(g[e], y[e], dot[j]);
       }
     }
-    if (a.gx) {
+    if (SPECIAL && a.gx && in) {
       u32x4 o;
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[e] = pack2g(gx[2 * e], gx[2 * e + 1]);
-      ((u32x4 *)(a.gx + (size_t)t * H))[ch] = o;
+      __builtin_nontemporal_store(o, (u32x4 *)(a.gx + (size_t)t * H) + ch);
     }
+  }
+  if (!SPECIAL && a.gx) {  // no copy and no constant experts: zeros
+    for (int ch = tid; ch < nch; ch += blockDim.x) ((u32x4 *)(a.gx + (size_t)t * H))[ch] = u32x4{0u, 0u, 0u, 0u};
   }
   if (a.gw) {
 #pragma unroll
@@ -119,7 +149,7 @@ __global__ void __launch_bounds__(THREADS) combine_grad_kernel(CombineGradArgs a
     __syncthreads();
     if (tid < K) {
       float s = 0.0f;
-      for (int v = 0; v < THREADS / 64; ++v) s += part[v][tid];
+      for (int v = 0; v < (int)(blockDim.x >> 6); ++v) s += part[v][tid];
       a.gw[(size_t)t * K + tid] = s;
     }
   }
@@ -167,9 +197,18 @@ __global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
   }
 }
 
+template <int KMAX, int U>
+static void launch_u(const CombineGradArgs &a, hipStream_t st) {
+  const int nch = a.c.H >> 3;
+  const dim3 grid((unsigned)a.c.T), block((unsigned)((nch + 64 * U - 1) / (64 * U) * 64));  // nch <= 1024
+  if (a.c.C + a.c.Kc > 0) hipLaunchKernelGGL((combine_grad_kernel<KMAX, U, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((combine_grad_kernel<KMAX, U, false>), grid, block, 0, st, a);
+}
+
 template <int KMAX>
 static void launch_k(const CombineGradArgs &a, hipStream_t st) {
-  hipLaunchKernelGGL((combine_grad_kernel<KMAX, 256>), dim3((unsigned)a.c.T), dim3(256), 0, st, a);
+  if (a.c.T <= 512) launch_u<KMAX, 1>(a, st);  // few workgroups: more threads in each
+  else launch_u<KMAX, 2>(a, st);
 }
 
 hipError_t launch_combine_grad(const CombineGradArgs &a, hipStream_t st) {

@@ -106,7 +106,7 @@ struct Tile {
   static_assert((!MCOL || BM >= 64) && (!NCOL || BN >= 128), "swz_col stays within a row");
   static_assert(FN % 2 == 0, "the epilogue stores 8 columns, or 4 with the gate");
   static_assert(!MX || BM % 64 == 0, "a load of scales is of one side");
-  static_assert(NST % 2 == 0 && (!MX || NST == 2), "scales are loaded one stage ahead of the first of their two");
+  static_assert(!MX || NST == 2, "scales are loaded one stage ahead of the first of their two");
 };
 
 // the n index (within the tile; for the gate: row of w relative to its half, and the half) of LDS row p
@@ -135,31 +135,30 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char *)lds;
 
   const int lane = tid & 63;
-  if (tid < 64) {  // tiles before each expert, 64 experts at a time
-    int base = 0;
-    const int most = (int)(a.g.rows / BM) + E;  // what ascending offsets give at most: keeps others in range
-    for (int e0 = 0; e0 < E; e0 += 64) {
-      int mine = 0;
-      if (e0 + lane < E) {
-        if (OP == OP_WGRAD) {
-          mine = (a.M + BM - 1) / BM;
-        } else {
+  const int wmt = (a.M + BM - 1) / BM;  // wgrad: tiles along m of every expert
+  if (OP != OP_WGRAD) {
+    if (tid < 64) {  // tiles before each expert, 64 experts at a time
+      int base = 0;
+      const int most = (int)(a.g.rows / BM) + E;  // what ascending offsets give at most: keeps others in range
+      for (int e0 = 0; e0 < E; e0 += 64) {
+        int mine = 0;
+        if (e0 + lane < E) {
           int64_t lo;
           int n;
           expert_rows(a.g, e0 + lane, lo, n);
           mine = (n + BM - 1) / BM;
         }
+        const int incl = wave_inclusive_sum(mine);
+        const int before = base + incl - mine;
+        if (e0 + lane < E) first[e0 + lane] = before > most ? most : before;
+        base += readlane(incl, 63);
+        if (base > most) base = most;
       }
-      const int incl = wave_inclusive_sum(mine);
-      const int before = base + incl - mine;
-      if (e0 + lane < E) first[e0 + lane] = OP != OP_WGRAD && before > most ? most : before;
-      base += readlane(incl, 63);
-      if (OP != OP_WGRAD && base > most) base = most;
+      if (lane == 0) first[E] = base;
     }
-    if (lane == 0) first[E] = base;
+    __syncthreads();
   }
-  __syncthreads();
-  const uint32_t tiles = (uint32_t)first[E] * (uint32_t)ntn;  // fits: see launch_cfg
+  const uint32_t tiles = (uint32_t)(OP == OP_WGRAD ? E * wmt : first[E]) * (uint32_t)ntn;  // fits: see launch_cfg
 
   // Workgroups go round the 8 XCDs, each with an L2 of its own: XCD x takes the x-th eighth of the tiles, its
   // workgroups neighbouring ones, so that those that run together share operands in that L2.
@@ -188,12 +187,19 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
   i32x4 mres, nres[C::HALVES];  // row operands: over the tile's rows
   auto enter = [&]() LAMBDA {
     const uint32_t mg = tile / (uint32_t)ntn;
-    int x = 0;  // the last expert whose tiles begin at or before mg: it has some
-    for (int step = 1024; step > 0; step >>= 1)
-      if (x + step < E && first[x + step] <= (int)mg) x += step;
-    e = __builtin_amdgcn_readfirstlane(x);
-    const int before = __builtin_amdgcn_readfirstlane(first[e]);
-    const int me = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
+    int before, me;
+    if (OP == OP_WGRAD) {
+      e = (int)(mg / (uint32_t)wmt);
+      before = e * wmt;
+      me = wmt;
+    } else {
+      int x = 0;  // the last expert whose tiles begin at or before mg: it has some
+      for (int step = 1024; step > 0; step >>= 1)
+        if (x + step < E && first[x + step] <= (int)mg) x += step;
+      e = __builtin_amdgcn_readfirstlane(x);
+      before = __builtin_amdgcn_readfirstlane(first[e]);
+      me = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
+    }
     // the expert's tiles in groups of up to kGroup along m, in each along m first
     const uint32_t rem = tile - (uint32_t)before * ntn, grp = rem / (uint32_t)(kGroup * ntn), in = rem - grp * kGroup * ntn;
     const uint32_t gm = me - grp * kGroup < kGroup ? me - grp * kGroup : kGroup, nt = in / gm;
@@ -364,9 +370,11 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
 
   // ---- a stage, in buffer b of the ring.  The products of one step of 64 bytes of k run while the next step's
   // operands come from LDS.  Before those are the next stage's, every wave has read this stage, so its buffer
-  // takes the loads of stage `ahead`, and the next stage's loads have to be there.  after: the next stage
-  auto stage = [&](auto b_, int after, int ahead) LAMBDA {
+  // takes the loads of stage `ahead`, and the next stage's loads have to be there.  after: the next stage.  A wave
+  // without rows (IDLE) only loads and waits.
+  auto stage = [&](auto b_, auto idle_, int after, int ahead) LAMBDA {
     constexpr int b = decltype(b_)::value, bn = (b + 1) % NST;
+    constexpr bool IDLE = decltype(idle_)::value;
     static_for<2>([&](auto ks_) LAMBDA {
       constexpr int ks = decltype(ks_)::value;
       if constexpr (ks == 1) {
@@ -378,10 +386,11 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
       }
       static_for<C::FM>([&](auto i_) LAMBDA {
         constexpr int i = decltype(i_)::value;
-        multiply(ks_, i_);
+        if constexpr (!IDLE) multiply(ks_, i_);
         if constexpr (ks == 1) {
           static_for_from<i * LOADS / C::FM, (i + 1) * LOADS / C::FM>([&](auto l_) LAMBDA { issue(ahead, b_, l_); });
         }
+        if constexpr (IDLE) return;
 #pragma unroll
         for (int j = i * C::FN / C::FM; j < (i + 1) * C::FN / C::FM; ++j) fb[ks ^ 1][j] = read_n(ks == 1 ? bn : b, j, ks ^ 1);
         fa[ks ^ 1][i] = read_m(ks == 1 ? bn : b, i, ks ^ 1);
@@ -428,8 +437,13 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
     if constexpr (!RING) begin();
     // whole turns of the buffers, so that each tile begins at the first: up to NST - 1 stages of zeros more
     const int turns = stages > NST ? (stages + NST - 1) / NST : 1, full = RING ? turns - 1 : turns;
-    for (int s0 = 0; s0 < full * NST; s0 += NST)
-      static_for<NST>([&](auto b_) LAMBDA { stage(b_, s0 + decltype(b_)::value + 1, s0 + decltype(b_)::value + NST); });
+    auto run = [&](auto idle_) LAMBDA {
+      for (int s0 = 0; s0 < full * NST; s0 += NST)
+        static_for<NST>([&](auto b_) LAMBDA { stage(b_, idle_, s0 + decltype(b_)::value + 1, s0 + decltype(b_)::value + NST); });
+    };
+    // a tile that ends before the wave's rows (in RING's last turn the products of such a wave are of no use)
+    if (WM > 1 && m0 + mfirst >= (OP == OP_WGRAD ? a.M : cnt)) run(std::true_type{});
+    else run(std::false_type{});
     const int m1 = m0, n1 = n0, e1 = e, mlim = OP == OP_WGRAD ? a.M : cnt;  // mlim: rows of the result
     const int64_t lo1 = lo;
     tile += per;
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
       if (tile < last) enter();  // else this one's again, for nothing
       static_for<NST>([&](auto b_) LAMBDA {
         constexpr int b = decltype(b_)::value;
-        stage(b_, b + 1 < NST ? (turns - 1) * NST + b + 1 : 0, b);
+        stage(b_, std::false_type{}, b + 1 < NST ? (turns - 1) * NST + b + 1 : 0, b);
       });
     } else {  // the next tile's first loads go out before this one's results
       stage_wait<0>();
@@ -454,7 +468,7 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
 
     // ---- results: lane (g, r16) holds, of row i * 16 + r16, 4 FN consecutive columns
     constexpr int F = GATED ? C::FN / 2 : C::FN;
-    const int l = lane, nl = n1 + wn * 16 * F + (l >> 4) * 4 * F;
+    const int nl = n1 + wn * 16 * F + g * 4 * F;
     float cs[TY == MOE_ROWS_INT8 ? 4 * C::FN : 1];  // the columns' scales
     if constexpr (TY == MOE_ROWS_INT8) {
 #pragma unroll
@@ -465,7 +479,7 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
     }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      const int m = m1 + mfirst + i * 16 + (l & 15);
+      const int m = m1 + mfirst + i * 16 + r16;
       if (m >= mlim) continue;
       const float rs = TY == MOE_ROWS_INT8 && a.ms ? ((const float *)a.ms)[lo1 + m] : 1.0f;
       float v[4 * C::FN];
@@ -516,23 +530,26 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
   hipLaunchKernelGGL(k, dim3(grid), dim3(C::T), lds, st, a);
   return hipGetLastError();
 }
-// The tile.  Figures: us on one MI355X, every operand from HBM; `mean` is rows per expert.
-//  16 x 64, 2 waves    forward, mean <= 16: weights streamed once, four or so workgroups a CU.  8 experts with a row,
-//                      4096 -> 2 x 1024 bf16: 22 against 28 (128 x 128)
-//  64 x 128, 4 waves   mean <= 64
-//  128 x 128, 4 waves, four stages     at most a tile a CU: depth counts.  8 x 128 rows, 7168 -> 2 x 2048 int8: 55
-//                      against 70 with two stages (two workgroups a CU), 91 with 256 x 256
-//  256 x 256, 8 waves  tiles for most CUs and long sums: 16 x 2048 rows, 4096 -> 4096: 881 against 1175 (128 x 128)
-//  128 x 128, two stages, two workgroups a CU     the rest
-// MXFP4 has two stages always (see Tile).
+// The tile.  Figures: us on one MI355X, every operand from HBM.
+//  16 x 64, 2 waves, four stages       forward with at most 16 rows an expert: weights streamed once, three workgroups
+//                      a CU.  8 rows of 8 experts, 4096 -> 2 x 1024 bf16: 22; 64 x 128: 23, 128 x 128: 28
+//  64 x 128, 4 waves, four stages      at most 64 rows an expert
+//  128 x 128, 4 waves, four stages     hardly more tiles than CUs: depth counts.  13 x 235 rows, dgrad 2056 -> 1048: 29
+//                      against 38 with two stages and two workgroups a CU, 59 with 256 x 256
+//  256 x 256, 8 waves, two stages      tiles for most CUs and long sums: 16 x 2048 rows, 4096 -> 4096 bf16: 881; 128 x
+//                      128: 1175, 128 x 256: 1200
+//  256 x 128, 8 waves, three stages    between them: the rows of an expert in one tile, its waves without rows idle.
+//                      1024 rows on 8 experts, 7168 -> 2 x 2048 int8: 58; 128 x 128: 76, 256 x 256: 92
+//  128 x 128, two stages, two workgroups a CU     the same for MXFP4, which has two stages always (see Tile)
 template <int TY, int OP, bool GATED, bool F32>
 static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
   constexpr bool MX = TY == MOE_ROWS_MXFP4;
   constexpr int DEEP = MX ? 2 : 4;
-  const int64_t mean = (a.g.rows + a.g.E - 1) / a.g.E, m = OP == OP_WGRAD ? a.M : mean;
+  const int64_t E = a.g.E, mean = (a.g.rows + E - 1) / E, m = OP == OP_WGRAD ? a.M : mean;
+  // tiles to expect: ragged rows leave half a tile an expert empty
   auto tiles = [&](int bm, int bn) {
     if (GATED) bn /= 2;
-    return a.g.E * ((m + bm - 1) / bm) * ((a.N + bn - 1) / bn);
+    return (OP == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm) * ((a.N + bn - 1) / bn);
   };
   if constexpr (MX) {
     if (a.K % 128 != 0) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, false>(a, st);
@@ -541,10 +558,13 @@ static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
     if (mean <= 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);
   }
   if (m <= 64) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, DEEP, true, true>(a, st);
-  if (!MX && tiles(128, 128) <= 256) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, DEEP, true, true>(a, st);
+  if constexpr (!MX) {
+    if (tiles(128, 128) <= 256) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, true>(a, st);
+  }
   if (tiles(256, 256) >= 200 && mean >= (OP == OP_WGRAD ? 512 : 128))
     return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, true>(a, st);
-  return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
+  if constexpr (MX) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
+  else return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, true>(a, st);
 }
 
 hipError_t launch_experts(const ExpertsArgs &a, int op, int row_type, int act, bool out_fp32, hipStream_t st) {
