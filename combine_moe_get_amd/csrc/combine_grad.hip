@@ -155,30 +155,57 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   }
 }
 
-// workgroup (64 columns, constant expert): 16 waves, wave v adds the slots of the v-th sixteenth of the tokens
+// workgroup (64 columns, constant expert): 16 waves, wave v adds the slots of the v-th sixteenth of the tokens, in
+// order.  A wave looks at 512 slots at a time (eight loads under way), lists the ones it is looking for in LDS and
+// takes eight of them at a time.
+constexpr int kScan = 512, kTake = 8;
 __global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;
+  __shared__ int slot[16][kScan];
   __shared__ float sg[16][64], sq[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int k = blockIdx.y, h = blockIdx.x * 64 + lane;
   const int id = c.E + c.Z + c.C + k;
-  const int per = (c.T + 15) / 16, lo = wave * per, hi = lo + per < c.T ? lo + per : c.T;
+  const int per = (c.T + 15) / 16, lo = wave * per < c.T ? wave * per : c.T, hi = lo + per < c.T ? lo + per : c.T;
+  const int s1 = hi * c.K;  // T K <= 2^24
   float g = 0.0f, q = 0.0f;
-  for (int64_t s0 = (int64_t)lo * c.K; s0 < (int64_t)hi * c.K; s0 += 64) {
-    const int64_t s = s0 + lane;
-    const bool in = s < (int64_t)hi * c.K;
-    bool hit = in && c.topk_idx[s] == id;
-    if (hit && c.mask) hit = c.mask[s / c.K] != 0;
-    const float w = hit ? c.w[s] : 0.0f;
-    uint64_t hits = ballot(hit);
-    while (hits) {
-      const int l = __builtin_ctzll(hits);
-      hits &= hits - 1;
-      if (h < c.H) {
-        const int64_t at = (s0 + l) / c.K * c.H + h;
-        const float wg = readlane_f(w, l) * __uint_as_float((uint32_t)a.go[at] << 16);
-        g += wg;
-        if (a.ga1) q = __builtin_fmaf(wg, __uint_as_float((uint32_t)c.ori_x[at] << 16), q);
+  for (int s0 = lo * c.K; s0 < s1; s0 += kScan) {
+    int ids[kScan / 64];
+#pragma unroll
+    for (int i = 0; i < kScan / 64; ++i) ids[i] = s0 + i * 64 + lane < s1 ? c.topk_idx[s0 + i * 64 + lane] : -1;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kScan / 64; ++i) {
+      const int s = s0 + i * 64 + lane;
+      bool hit = ids[i] == id;
+      if (hit && c.mask) hit = c.mask[s / c.K] != 0;
+      const uint64_t hits = ballot(hit);
+      if (hit) slot[wave][n + popc_below(hits)] = s;
+      n += __builtin_popcountll(hits);
+    }
+    // the list is the wave's own: its LDS accesses are in order
+    for (int i = 0; i < n; i += kTake) {
+      float w[kTake], gv[kTake], xv[kTake];
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        w[u] = gv[u] = xv[u] = 0.0f;
+        if (i + u < n) {
+          const int s = __builtin_amdgcn_readfirstlane(slot[wave][i + u]);
+          w[u] = c.w[s];
+          if (h < c.H) {
+            const size_t at = (size_t)(s / c.K) * c.H + h;
+            gv[u] = __uint_as_float((uint32_t)a.go[at] << 16);
+            if (a.ga1) xv[u] = __uint_as_float((uint32_t)c.ori_x[at] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        if (i + u < n) {
+          const float wg = w[u] * gv[u];
+          g += wg;
+          q = __builtin_fmaf(wg, xv[u], q);
+        }
       }
     }
   }

@@ -74,23 +74,36 @@ class ExpertsCall(B.PreparedCall):
     __slots__ = ("_device",)
 
     def __init__(self, fn, args, what, keep, result, device):
-        super().__init__(fn, args, what, keep, result)
+        self._fn, self._args, self._what, self._keep, self.result = fn, args, what, keep, result
         self._device = device
 
     def __call__(self, stream=None):
         if stream is not None and stream.device != self._device:
             raise ValueError(f"{self._what}: the stream is on {stream.device}, the tensors on {self._device}")
-        if torch.cuda.current_device() == self._device.index:
-            return super().__call__(stream)
-        with torch.cuda.device(self._device):
-            return super().__call__(stream)
+        if torch.cuda.current_device() != self._device.index:
+            with torch.cuda.device(self._device):
+                return self._run(stream)
+        return self._run(stream)
+
+    def _run(self, stream):
+        s = torch.cuda.current_stream(self._device) if stream is None else stream
+        self._args[-1] = s.cuda_stream
+        st = self._fn(*self._args)
+        if st != B.MOE_OK:
+            raise B.MoeGetError(self._what, st)
+        return self.result
 
 
 def _ptr(t, name, dtypes, numel, device, required=True):
-    p = B._ptr(t, name, dtypes, numel, required)
-    if t is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, other tensors of the call on {device}")
-    return p
+    """Address of a tensor that is fit for the call, or None for an optional or empty one."""
+    if t is None and not required:
+        return None
+    # everything in order: the case that calls spend their time on
+    if (isinstance(t, torch.Tensor) and t.device == device and t.dtype in dtypes and t.is_contiguous()
+            and (numel is None or t.numel() >= numel)):
+        return t.data_ptr() or None
+    B._ptr(t, name, dtypes, numel, required)  # says what is wrong
+    raise ValueError(f"{name} is on {t.device}, other tensors of the call on {device}")
 
 
 def _checked(shape, row_type, what):
@@ -100,6 +113,8 @@ def _checked(shape, row_type, what):
 
 
 def _device_of(t, name):
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        return t.device
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
