@@ -77,11 +77,11 @@ __device__ __forceinline__ float silu(float g) {
 // cycle serves (128 bytes) fall on different banks.
 // Row operands: one chunk of each of 8 rows of 128 bytes.
 __device__ __forceinline__ int swz_row(int row) { return row & 7; }
-// Column operands: four rows of k (k & 3; on the m side 32 bytes of each, on the n side four pieces of 8 bytes,
-// 32 bytes apart).
-template <bool NSIDE>
+// Column operands: four rows of k (k & 3); on the m side 32 bytes of each, on the n side (FN > 0: see n_of) four
+// pieces of 8 bytes, FN / 2 chunks apart.
+template <int FN>
 __device__ __forceinline__ int swz_col(int k) {
-  return NSIDE ? (k & 1) | ((k & 2) << 2) : (k & 3) << 1;
+  return FN == 0 ? (k & 3) << 1 : FN == 2 ? (k & 3) << 2 : FN == 4 ? (k & 1) | ((k & 2) << 2) : k & 3;
 }
 
 // TY: row type; BM x BN: the tile (with the gate: BN / 2 columns of the result); WM x WN: its waves;
@@ -123,7 +123,7 @@ __device__ __forceinline__ int n_of(int p, int &half) {
 #define LAMBDA __attribute__((always_inline))
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
-__global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) {
+__global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 1 : 2) experts_kernel(ExpertsArgs a) {
   using C = Tile<TY, OP, GATED, BM, BN, WM, WN, NST>;
   constexpr bool MX = C::MX;
   extern __shared__ __align__(1024) char lds[];
@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
       before = e * wmt;
       me = wmt;
     } else {
-      int x = 0;  // the last expert whose tiles begin at or before mg: it has some
-      for (int step = 1024; step > 0; step >>= 1)
-        if (x + step < E && first[x + step] <= (int)mg) x += step;
-      e = __builtin_amdgcn_readfirstlane(x);
+      // the last expert whose tiles begin at or before mg (it has some): 64 experts compared at once
+      const int each = (E + 63) / 64;
+      const int blk = __builtin_popcountll(ballot(lane * each < E && first[lane * each] <= (int)mg)) - 1;
+      const int x = blk * each + lane;
+      e = blk * each + __builtin_popcountll(ballot(lane < each && x < E && first[x] <= (int)mg)) - 1;
       before = __builtin_amdgcn_readfirstlane(first[e]);
       me = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
     }
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
     for (int i = 0; i < C::AI; ++i) {
       const int p = (wave * C::AI + i) * 64 + lane;
       if (C::MCOL) {
-        const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<false>(k);
+        const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<0>(k);
         ao[i] = m0 + c * 8 < a.M ? (uint32_t)(k * (int)mrow + c * 16) : kOut;
       } else {
         ao[i] = m0 + p / 8 < cnt ? (uint32_t)(p / 8 * (int)mrow + c16) : kOut;
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
     for (int i = 0; i < C::BI; ++i) {
       const int p = (wave * C::BI + i) * 64 + lane;
       if (C::NCOL) {
-        const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<true>(k);
+        const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<C::FN>(k);
         bo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * (int)nrow + c * 16) : kOut;
       } else {
         int half;
@@ -316,8 +317,8 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
     na[ks] = lds0 + NST * C::ABYTES + nfirst * kKB + piece;
   }
   // columns: swz_col looks only at bits of k that ks and u leave alone
-  if (C::MCOL) ma[0] = lds0 + kt * BM * 2 + ((((mfirst + (lane & 3) * 4) >> 3) ^ swz_col<false>(kt)) << 4) + (lane & 1) * 8;
-  if (C::NCOL) na[0] = lds0 + NST * C::ABYTES + kt * BN * 2 + (((nfirst + (lane & 3) * 4 * C::FN) >> 3 ^ swz_col<true>(kt)) << 4);
+  if (C::MCOL) ma[0] = lds0 + kt * BM * 2 + ((((mfirst + (lane & 3) * 4) >> 3) ^ swz_col<0>(kt)) << 4) + (lane & 1) * 8;
+  if (C::NCOL) na[0] = lds0 + NST * C::ABYTES + kt * BN * 2 + (((nfirst + (lane & 3) * 4 * C::FN) >> 3 ^ swz_col<C::FN>(kt)) << 4);
   uint32_t sm = lds0 + NST * C::STAGE + (mfirst + r16) * 16 + g * 2, sn = sm + (BM + nfirst - mfirst) * 16;  // scales
   asm volatile("" : "+v"(ma[0]), "+v"(ma[1]), "+v"(na[0]), "+v"(na[1]), "+v"(sm), "+v"(sn));
   auto column = [&](uint32_t at, int R) LAMBDA {  // 8 rows of k, four columns of each
@@ -388,7 +389,8 @@ __global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) 
         constexpr int i = decltype(i_)::value;
         if constexpr (!IDLE) multiply(ks_, i_);
         if constexpr (ks == 1) {
-          static_for_from<i * LOADS / C::FM, (i + 1) * LOADS / C::FM>([&](auto l_) LAMBDA { issue(ahead, b_, l_); });
+          constexpr int l0 = 2 * i * LOADS / C::FM, l1 = 2 * (i + 1) * LOADS / C::FM;  // all in the first half
+          static_for_from<(l0 < LOADS ? l0 : LOADS), (l1 < LOADS ? l1 : LOADS)>([&](auto l_) LAMBDA { issue(ahead, b_, l_); });
         }
         if constexpr (IDLE) return;
 #pragma unroll
