@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
   // workgroups neighbouring ones, so that those that run together share operands in that L2.
   const uint32_t xcd = blockIdx.x & 7, per = (gridDim.x + 7 - xcd) >> 3;  // its workgroups
   const uint32_t last = (uint32_t)((uint64_t)tiles * (xcd + 1) / 8);
-  uint32_t tile = (uint32_t)((uint64_t)tiles * xcd / 8) + (blockIdx.x >> 3);
+  // In each round the workgroups' places are turned, so that an expert's last, short tile along m meets others.
+  constexpr uint32_t kTurn = 13;
+  uint32_t round = (uint32_t)((uint64_t)tiles * xcd / 8), place = blockIdx.x >> 3, tile = round + place;
   if (tile >= last) return;
 
   // byte strides of the operands' rows
@@ -448,7 +450,10 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     else run(std::false_type{});
     const int m1 = m0, n1 = n0, e1 = e, mlim = OP == OP_WGRAD ? a.M : cnt;  // mlim: rows of the result
     const int64_t lo1 = lo;
-    tile += per;
+    round += per;
+    place += kTurn % per;
+    if (place >= per) place -= per;
+    tile = round + place;
     if constexpr (RING) {  // the last turn loads the next tile's first stages
       if (tile < last) enter();  // else this one's again, for nothing
       static_for<NST>([&](auto b_) LAMBDA {
@@ -554,7 +559,9 @@ static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
     return (OP == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm) * ((a.N + bn - 1) / bn);
   };
   if constexpr (MX) {
-    if (a.K % 128 != 0) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, false>(a, st);
+    // rows of scales that do not begin at multiples of four bytes are copied byte by byte
+    if (a.K % 128 != 0 || (((uintptr_t)a.ms | (uintptr_t)a.ns) & 3) != 0)
+      return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, false>(a, st);
   }
   if constexpr (OP == OP_FORWARD && !MX) {
     if (mean <= 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);

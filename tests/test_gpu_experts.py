@@ -107,22 +107,65 @@ def test_mxfp4(counts, K, N, gated):
     X.check(out, ref, tol, rows.used, "mxfp4")
 
 
+@pytest.mark.parametrize("K", [320, 384, 640])  # the last with scales that fill 16 bytes a row and a part
 @pytest.mark.parametrize("rows_of", [1, 40, 200])
-def test_mxfp4_nan_scale_reaches_its_own_sums_only(rows_of):
-    K, N = 320, 72
+def test_mxfp4_nan_scale_reaches_its_own_sums_only(rows_of, K):
+    N = 72
     r = np.random.default_rng(4)
     t = torch.from_numpy
     x, w = r.integers(0, 256, (rows_of, K // 2)).astype(np.uint8), r.integers(0, 256, (1, N, K // 2)).astype(np.uint8)
     xs, ws = np.full((rows_of, K // 32), 127, np.uint8), np.full((1, N, K // 32), 120, np.uint8)
-    xs[rows_of // 2, 9] = 255  # the last block of a row
+    xs[rows_of // 2, -1] = 255  # the last block of a row
+    xs[rows_of // 3, 0] = 255   # the first of another
     ws[0, 5, 3] = 255
+    ws[0, 9, 0] = 255
     off = torch.tensor([0, rows_of], dtype=torch.int32, device=X.DEV)
     out = mg.experts_matmul(mg.make_experts_shape(rows_of, 1, K, N), t(x).to(X.DEV), t(w).to(X.DEV), off, t(xs).to(X.DEV),
                             t(ws).to(X.DEV)).cpu()
     nan = torch.zeros(rows_of, N, dtype=torch.bool)
-    nan[rows_of // 2] = True
-    nan[:, 5] = True
+    nan[[rows_of // 2, rows_of // 3]] = True
+    nan[:, [5, 9]] = True
     assert torch.equal(torch.isnan(out), nan)
+
+
+def test_mxfp4_scales_at_odd_addresses():
+    K, N, rows = 256, 136, 70
+    r = np.random.default_rng(13)
+    t = torch.from_numpy
+    x, w = r.integers(0, 256, (rows, K // 2)).astype(np.uint8), r.integers(0, 256, (1, N, K // 2)).astype(np.uint8)
+    xs, ws = r.integers(121, 131, (rows, K // 32)).astype(np.uint8), r.integers(112, 120, (1, N, K // 32)).astype(np.uint8)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=X.DEV)
+    shape, xd, wd = mg.make_experts_shape(rows, 1, K, N), t(x).to(X.DEV), t(w).to(X.DEV)
+    want = mg.experts_matmul(shape, xd, wd, off, t(xs).to(X.DEV), t(ws).to(X.DEV))
+
+    def odd(a, by):  # the same values, `by` bytes behind an aligned address
+        buf = torch.empty(a.size + by, dtype=torch.uint8, device=X.DEV)
+        buf[by:] = t(a).flatten().to(X.DEV)
+        return buf[by:].view(a.shape)
+
+    for i, j in ((1, 0), (0, 3), (2, 1)):
+        assert torch.equal(mg.experts_matmul(shape, xd, wd, off, odd(xs, i), odd(ws, j)), want)
+
+
+def test_misaligned_rows_are_refused():
+    s = mg.make_experts_shape(4, 1, 64, 24)
+    x = torch.zeros(4 * 64 + 4, dtype=torch.bfloat16, device=X.DEV)[4:].view(4, 64)
+    w = torch.zeros(1, 24, 64, dtype=torch.bfloat16, device=X.DEV)
+    off = torch.tensor([0, 4], dtype=torch.int32, device=X.DEV)
+    with pytest.raises(mg.MoeGetError):
+        mg.experts_matmul(s, x, w, off)
+    with pytest.raises(ValueError, match="contiguous"):
+        mg.experts_matmul(s, torch.zeros(64, 4, dtype=torch.bfloat16, device=X.DEV).t(), w, off)
+    with pytest.raises(ValueError, match="elements"):
+        mg.experts_matmul(s, torch.zeros(3, 64, dtype=torch.bfloat16, device=X.DEV), w, off)
+    with pytest.raises(TypeError):
+        mg.experts_matmul(s, w.view(24, 64)[:4].float(), w, off)
+    with pytest.raises(TypeError):
+        mg.experts_matmul(s, w.view(24, 64)[:4], w, off.long())
+    with pytest.raises(ValueError, match="scales"):
+        mg.experts_matmul(s, w.view(24, 64)[:4], w, off, row_scales=torch.ones(4, device=X.DEV))
+    with pytest.raises(ValueError, match="device"):
+        mg.experts_matmul(s, w.view(24, 64)[:4], w, off.cpu())
 
 
 @pytest.mark.parametrize("rows_of", [1, 40, 200])
@@ -321,6 +364,43 @@ def test_offsets_that_make_no_sense_touch_nothing_outside(off, stride):
     for t in (out, dx):
         assert torch.all(t[:2] == -7) and torch.all(t[-2:] == -7)
     assert torch.all((dw >= 0) & (dw <= rows))
+
+
+def test_beyond_4_gib():
+    """Rows and weights whose byte offsets pass 32 bits: the last window's rows, the last expert's weights."""
+    K, N, E, stride = 8192, 8192, 40, 7500
+    counts = [2] + [0] * (E - 2) + [21]
+    r = np.random.default_rng(14)
+    rows = E * stride  # 4.9 GB of bf16
+    shape = mg.make_experts_shape(rows, E, K, N, E, stride)
+    off = torch.from_numpy(X.offsets(counts)).to(X.DEV)
+    lo = (E - 1) * stride
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device=X.DEV)
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device=X.DEV)  # 5.4 GB
+    assert x.numel() * 2 > 1 << 32 and w.numel() * 2 > 1 << 32
+    x1, w1, dy1 = X.bf16(r, 21, K), X.bf16(r, N, K, scale=K ** -0.5), X.bf16(r, 21, N)
+    x[lo:lo + 21], w[-1] = x1.to(X.DEV), w1.to(X.DEV)
+    one = X.Rows([21], extra=0)
+    out = torch.zeros(rows, N, dtype=torch.bfloat16, device=X.DEV)
+    mg.experts_matmul(shape, x, w, off, out=out)
+    ref, tol = X.product(one, X.f64(x1), X.f64(w1)[None], False)
+    X.check(out[lo:lo + 21], ref, tol, one.used, "forward")
+    assert not out[lo + 21:].any() and not out[:lo].any()
+    out[lo:lo + 21] = dy1.to(X.DEV)
+    dx = mg.experts_matmul_dgrad(shape, out, w, off, out=torch.zeros_like(x))
+    ref, tol = X.product(one, X.f64(dy1), X.f64(w1).T[None], False)
+    X.check(dx[lo:lo + 21], ref, tol, one.used, "dgrad")
+    del dx
+    dw = mg.experts_matmul_wgrad(shape, out, x, off, out=w)
+    a, b = X.f64(dy1), X.f64(x1)
+    err = 29 * X.STEP32 * (np.abs(a).T @ np.abs(b))
+    X.check(dw[-1], a.T @ b, err + X.BF16_HALF * (np.abs(a.T @ b) + err) + X.TINY, np.ones(N, bool), "wgrad")
+    assert not dw[:-1].any()
+    del dw, w, out
+    for row_type in (mg.ROWS_INT8, mg.ROWS_MXFP4):
+        codes, scales = mg.quantize_rows(x, row_type)
+        want = mg.quantize_rows(x1.to(X.DEV), row_type)
+        assert torch.equal(codes[lo:lo + 21], want[0]) and torch.equal(scales[lo:lo + 21], want[1])
 
 
 def test_no_rows():
