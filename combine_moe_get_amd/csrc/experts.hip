@@ -77,20 +77,23 @@ __device__ __forceinline__ float silu(float g) {
 // cycle serves (128 bytes) fall on different banks.
 // Row operands: one chunk of each of 8 rows of 128 bytes.
 __device__ __forceinline__ int swz_row(int row) { return row & 7; }
-// Column operands: four rows of k (k & 3); on the m side 32 bytes of each, on the n side (FN > 0: see n_of) four
-// pieces of 8 bytes, FN / 2 chunks apart.
-template <int FN>
+// Column operands: four rows of k (k & 3), 32 bytes of each, or on the n side with G = 2 (see n_of) four pieces of
+// 8 bytes, a chunk apart.
+template <int G>
 __device__ __forceinline__ int swz_col(int k) {
-  return FN == 0 ? (k & 3) << 1 : FN == 2 ? (k & 3) << 2 : FN == 4 ? (k & 1) | ((k & 2) << 2) : k & 3;
+  return (k & 3) << G;
 }
 
 // TY: row type; BM x BN: the tile (with the gate: BN / 2 columns of the result); WM x WN: its waves;
 // NST: stages in LDS; WIDE: MXFP4 scales of a row begin at multiples of four bytes
-template <int TY, int OP, bool GATED, int BM, int BN, int WM, int WN, int NST>
+template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST>
 struct Tile {
   static constexpr int W = WM * WN, T = 64 * W;               // waves, threads
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 results of a wave
   static constexpr int CO = GATED ? BN / 2 : BN;              // result columns
+  // 16-column results of a wave per half; and how many of them are interleaved, so that a lane, which holds four
+  // consecutive columns of each, stores 16 bytes and four lanes 64 in a row (see n_of)
+  static constexpr int F = GATED ? FN / 2 : FN, G = F32 || F < 2 ? 1 : 2;
   static constexpr bool MCOL = OP == OP_WGRAD, NCOL = OP != OP_FORWARD, MX = TY == MOE_ROWS_MXFP4;
   static constexpr int ABYTES = BM * kKB, BBYTES = BN * kKB, STAGE = ABYTES + BBYTES;
   static constexpr int AI = ABYTES / 1024 / W, BI = BBYTES / 1024 / W;  // loads of a wave per stage
@@ -104,27 +107,25 @@ struct Tile {
   static constexpr int HALVES = GATED && BI > FN ? 2 : 1;
   static_assert(!GATED || FN % BI == 0 || BI == 2 * FN, "a load is of one half");
   static_assert((!MCOL || BM >= 64) && (!NCOL || BN >= 128), "swz_col stays within a row");
-  static_assert(FN % 2 == 0, "the epilogue stores 8 columns, or 4 with the gate");
+  static_assert(F % G == 0 && (!GATED || FN % 2 == 0), "whole groups of results");
   static_assert(!MX || BM % 64 == 0, "a load of scales is of one side");
   static_assert(!MX || NST == 2, "scales are loaded one stage ahead of the first of their two");
 };
 
-// the n index (within the tile; for the gate: row of w relative to its half, and the half) of LDS row p
-// of the n side.  A wave's FN results of 16 columns are interleaved so that a lane, which holds four
-// consecutive columns of each, holds 4 FN consecutive ones in all.
-template <class C, bool GATED>
+// the n index (within the tile; for the gate: row of w relative to its half, and the half) of LDS row p of the n side:
+// of row r of result f of a wave, results interleaved by G
+template <class C>
 __device__ __forceinline__ int n_of(int p, int &half) {
-  constexpr int F = GATED ? C::FN / 2 : C::FN;
-  const int b = p / (16 * C::FN), q = p % (16 * C::FN), f = q / 16, r = q % 16;
-  half = GATED ? f / F : 0;
-  return b * 16 * F + (r / 4) * 4 * F + (f % F) * 4 + (r % 4);
+  const int b = p / (16 * C::FN), q = p % (16 * C::FN), f = q / 16 % C::F, r = q % 16;
+  half = q / 16 / C::F;
+  return b * 16 * C::F + f / C::G * 16 * C::G + r / 4 * 4 * C::G + f % C::G * 4 + r % 4;
 }
 
 #define LAMBDA __attribute__((always_inline))
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
 __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 1 : 2) experts_kernel(ExpertsArgs a) {
-  using C = Tile<TY, OP, GATED, BM, BN, WM, WN, NST>;
+  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST>;
   constexpr bool MX = C::MX;
   extern __shared__ __align__(1024) char lds[];
   int *first = (int *)(lds + C::LDS);  // [E + 1] tiles along m before each expert
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     for (int i = 0; i < C::AI; ++i) {
       const int p = (wave * C::AI + i) * 64 + lane;
       if (C::MCOL) {
-        const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<0>(k);
+        const int k = p / (BM / 8), c = (p % (BM / 8)) ^ swz_col<1>(k);
         ao[i] = m0 + c * 8 < a.M ? (uint32_t)(k * (int)mrow + c * 16) : kOut;
       } else {
         ao[i] = m0 + p / 8 < cnt ? (uint32_t)(p / 8 * (int)mrow + c16) : kOut;
@@ -229,11 +230,11 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     for (int i = 0; i < C::BI; ++i) {
       const int p = (wave * C::BI + i) * 64 + lane;
       if (C::NCOL) {
-        const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<C::FN>(k);
+        const int k = p / (BN / 8), c = (p % (BN / 8)) ^ swz_col<C::G>(k);
         bo[i] = n0 + c * 8 < a.N ? (uint32_t)(k * (int)nrow + c * 16) : kOut;
       } else {
         int half;
-        const int n = n_of<C, GATED>(p / 8, half);
+        const int n = n_of<C>(p / 8, half);
         bo[i] = n0 + n < a.N ? (uint32_t)(n * (int)nrow + c16) : kOut;
       }
     }
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
           so[i] = m0 + p < cnt ? (uint32_t)(p * sw) : kOut;
         } else if (p < BM + BN) {
           int half;
-          const int n = n_of<C, GATED>(p - BM, half);
+          const int n = n_of<C>(p - BM, half);
           so[i] = n0 + n < a.N ? (uint32_t)((n + (GATED && half ? a.N : 0)) * sw) : kOut;
         } else {
           so[i] = kOut;
@@ -319,8 +320,8 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     na[ks] = lds0 + NST * C::ABYTES + nfirst * kKB + piece;
   }
   // columns: swz_col looks only at bits of k that ks and u leave alone
-  if (C::MCOL) ma[0] = lds0 + kt * BM * 2 + ((((mfirst + (lane & 3) * 4) >> 3) ^ swz_col<0>(kt)) << 4) + (lane & 1) * 8;
-  if (C::NCOL) na[0] = lds0 + NST * C::ABYTES + kt * BN * 2 + (((nfirst + (lane & 3) * 4 * C::FN) >> 3 ^ swz_col<C::FN>(kt)) << 4);
+  if (C::MCOL) ma[0] = lds0 + kt * BM * 2 + ((((mfirst + (lane & 3) * 4) >> 3) ^ swz_col<1>(kt)) << 4) + (lane & 1) * 8;
+  if (C::NCOL) na[0] = lds0 + NST * C::ABYTES + kt * BN * 2 + (((nfirst + (lane & 3) * 4 * C::G) >> 3 ^ swz_col<C::G>(kt)) << 4) + (C::G == 1 ? (lane & 1) * 8 : 0);
   uint32_t sm = lds0 + NST * C::STAGE + (mfirst + r16) * 16 + g * 2, sn = sm + (BM + nfirst - mfirst) * 16;  // scales
   asm volatile("" : "+v"(ma[0]), "+v"(ma[1]), "+v"(na[0]), "+v"(na[1]), "+v"(sm), "+v"(sn));
   auto column = [&](uint32_t at, int R) LAMBDA {  // 8 rows of k, four columns of each
@@ -335,7 +336,8 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     return *(__attribute__((address_space(3))) const i32x4 *)(uintptr_t)(ma[ks] + b * C::ABYTES + i * 16 * kKB);
   };
   auto read_n = [&](int b, int j, int ks) LAMBDA -> i32x4 {
-    if (C::NCOL) return column((na[0] ^ ((j >> 1) << 4)) + (j & 1) * 8 + b * C::BBYTES + ks * 8 * BN * 2, BN);
+    if (C::NCOL)
+      return column((na[0] ^ ((j / C::G) << (4 + C::G))) + j % C::G * 8 + b * C::BBYTES + ks * 8 * BN * 2, BN);
     return *(__attribute__((address_space(3))) const i32x4 *)(uintptr_t)(na[ks] + b * C::BBYTES + j * 16 * kKB);
   };
   // MXFP4: the scale bytes of the lane's two pieces of stage s (even: b = 0), of two rows in one register
@@ -473,14 +475,14 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) asm volatile("" : "+v"(acc[i][j]));
 
-    // ---- results: lane (g, r16) holds, of row i * 16 + r16, 4 FN consecutive columns
-    constexpr int F = GATED ? C::FN / 2 : C::FN;
-    const int nl = n1 + wn * 16 * F + g * 4 * F;
+    // ---- results: lane (g, r16) holds, of row i * 16 + r16, 4 G consecutive columns for each G results
+    constexpr int F = C::F, G = C::G;
+    const int nl = n1 + wn * 16 * F + g * 4 * G;
     float cs[TY == MOE_ROWS_INT8 ? 4 * C::FN : 1];  // the columns' scales
     if constexpr (TY == MOE_ROWS_INT8) {
 #pragma unroll
       for (int q = 0; q < 4 * C::FN; ++q) {
-        const int n = nl + q % (4 * F);
+        const int f = q / 4 % F, n = nl + f / G * 16 * G + f % G * 4 + q % 4;
         cs[q] = a.ns && n < a.N ? ((const float *)a.ns)[(int64_t)e1 * nw + n + (q >= 4 * F ? a.N : 0)] : 1.0f;
       }
     }
@@ -499,23 +501,15 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 #pragma unroll
         for (int q = 0; q < 4 * F; ++q) v[q] = silu(v[q]) * v[4 * F + q];
       }
-      const int64_t row = (OP == OP_WGRAD ? (int64_t)e1 * a.M : lo1) + m;
-      if constexpr (F == 1) {  // four columns
-        static_assert(!F32, "");
-        if (nl < a.N) *(u32x2 *)((uint16_t *)a.out + row * a.N + nl) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-      } else {
+      const int64_t at = ((OP == OP_WGRAD ? (int64_t)e1 * a.M : lo1) + m) * a.N + nl;
 #pragma unroll
-        for (int q = 0; q < 4 * F; q += 8) {
-          if (nl + q >= a.N) continue;  // N is a multiple of 8
-          if constexpr (F32) {
-            f32x4 *o = (f32x4 *)((float *)a.out + row * a.N + nl + q);
-            o[0] = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
-            o[1] = f32x4{v[q + 4], v[q + 5], v[q + 6], v[q + 7]};
-          } else {
-            *(u32x4 *)((uint16_t *)a.out + row * a.N + nl + q) =
-                u32x4{pack2(v[q], v[q + 1]), pack2(v[q + 2], v[q + 3]), pack2(v[q + 4], v[q + 5]), pack2(v[q + 6], v[q + 7])};
-          }
-        }
+      for (int f = 0; f < F; f += G) {
+        const int n = f * 16;
+        if (nl + n >= a.N) continue;  // N is a multiple of 8
+        const float *y = v + f * 4;
+        if constexpr (F32) *(f32x4 *)((float *)a.out + at + n) = f32x4{y[0], y[1], y[2], y[3]};
+        else if constexpr (G == 1) *(u32x2 *)((uint16_t *)a.out + at + n) = u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])};
+        else *(u32x4 *)((uint16_t *)a.out + at + n) = u32x4{pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
       }
     }
     if (tile >= last) break;
@@ -526,7 +520,7 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
 static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
-  using C = Tile<TY, OP, GATED, BM, BN, WM, WN, NST>;
+  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST>;
   // at most (2^27 / 64 + 2^11) * 2^10 or 2^21 * 2^10 tiles: below 2^32
   const int64_t mt = OP == OP_WGRAD ? (int64_t)a.g.E * ((a.M + BM - 1) / BM) : a.g.rows / BM + a.g.E;
   const int64_t tiles = mt * ((a.N + C::CO - 1) / C::CO);
