@@ -159,15 +159,23 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     }
     __syncthreads();
   }
-  const uint32_t tiles = (uint32_t)(OP == OP_WGRAD ? E * wmt : first[E]) * (uint32_t)ntn;  // fits: see launch_cfg
 
-  // Workgroups go round the 8 XCDs, each with an L2 of its own: XCD x takes the x-th eighth of the tiles, its
-  // workgroups neighbouring ones, so that those that run together share operands in that L2.
+  // Workgroups go round the 8 XCDs, each with an L2 of its own: an XCD's workgroups take neighbouring tiles, so that
+  // those that run together share operands in that L2.  Forward and dgrad: XCD x takes the x-th eighth of all tiles.
+  // wgrad, where a tile costs what its expert has rows: the x-th eighth of each expert's, if it has 64 or more.
   const uint32_t xcd = blockIdx.x & 7, per = (gridDim.x + 7 - xcd) >> 3;  // its workgroups
-  const uint32_t last = (uint32_t)((uint64_t)tiles * (xcd + 1) / 8);
+  const uint32_t each = (uint32_t)wmt * (uint32_t)ntn;                    // wgrad: tiles of an expert
+  const bool split = OP == OP_WGRAD && each >= 64;
+  const uint32_t mine0 = split ? each * xcd / 8 : 0, mine = split ? each * (xcd + 1) / 8 - mine0 : each;
+  uint32_t round = 0, last = mine * (uint32_t)E;  // fits: see launch_cfg
+  if (!split) {
+    const uint64_t tiles = OP == OP_WGRAD ? last : (uint64_t)(uint32_t)first[E] * (uint32_t)ntn;
+    round = (uint32_t)(tiles * xcd / 8);
+    last = (uint32_t)(tiles * (xcd + 1) / 8);
+  }
   // In each round the workgroups' places are turned, so that an expert's last, short tile along m meets others.
   constexpr uint32_t kTurn = 13;
-  uint32_t round = (uint32_t)((uint64_t)tiles * xcd / 8), place = blockIdx.x >> 3, tile = round + place;
+  uint32_t place = blockIdx.x >> 3, tile = round + place;
   if (tile >= last) return;
 
   // byte strides of the operands' rows
@@ -189,23 +197,25 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
   int sbytes[MX ? C::SI : 1];
   i32x4 mres, nres[C::HALVES];  // row operands: over the tile's rows
   auto enter = [&]() LAMBDA {
-    const uint32_t mg = tile / (uint32_t)ntn;
-    int before, me;
+    int me;
+    uint32_t rem;  // the expert's tiles along m, and which of its tiles this is
     if (OP == OP_WGRAD) {
-      e = (int)(mg / (uint32_t)wmt);
-      before = e * wmt;
+      e = (int)(tile / mine);
       me = wmt;
+      rem = mine0 + tile - (uint32_t)e * mine;
     } else {
       // the last expert whose tiles begin at or before mg (it has some): 64 experts compared at once
-      const int each = (E + 63) / 64;
-      const int blk = __builtin_popcountll(ballot(lane * each < E && first[lane * each] <= (int)mg)) - 1;
-      const int x = blk * each + lane;
-      e = blk * each + __builtin_popcountll(ballot(lane < each && x < E && first[x] <= (int)mg)) - 1;
-      before = __builtin_amdgcn_readfirstlane(first[e]);
+      const uint32_t mg = tile / (uint32_t)ntn;
+      const int step = (E + 63) / 64;
+      const int blk = __builtin_popcountll(ballot(lane * step < E && first[lane * step] <= (int)mg)) - 1;
+      const int x = blk * step + lane;
+      e = blk * step + __builtin_popcountll(ballot(lane < step && x < E && first[x] <= (int)mg)) - 1;
+      const int before = __builtin_amdgcn_readfirstlane(first[e]);
       me = __builtin_amdgcn_readfirstlane(first[e + 1]) - before;
+      rem = tile - (uint32_t)before * ntn;
     }
     // the expert's tiles in groups of up to kGroup along m, in each along m first
-    const uint32_t rem = tile - (uint32_t)before * ntn, grp = rem / (uint32_t)(kGroup * ntn), in = rem - grp * kGroup * ntn;
+    const uint32_t grp = rem / (uint32_t)(kGroup * ntn), in = rem - grp * kGroup * ntn;
     const uint32_t gm = me - grp * kGroup < kGroup ? me - grp * kGroup : kGroup, nt = in / gm;
     expert_rows(a.g, e, lo, cnt);
     m0 = (int)(grp * kGroup + in - nt * gm) * BM;
@@ -541,7 +551,8 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
 //                      128: 1175, 128 x 256: 1200
 //  256 x 128, 8 waves, three stages    between them: the rows of an expert in one tile, its waves without rows idle.
 //                      1024 rows on 8 experts, 7168 -> 2 x 2048 int8: 58; 128 x 128: 76, 256 x 256: 92
-//  128 x 128, two stages, two workgroups a CU     the same for MXFP4, which has two stages always (see Tile)
+//  128 x 128, two stages, two workgroups a CU     the same for wgrad (13 x 235 rows: 35 against 41) and for MXFP4,
+//                      which has two stages always (see Tile)
 template <int TY, int OP, bool GATED, bool F32>
 static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
   constexpr bool MX = TY == MOE_ROWS_MXFP4;
@@ -564,9 +575,9 @@ static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
   if constexpr (!MX) {
     if (tiles(128, 128) <= 256) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, true>(a, st);
   }
-  if (tiles(256, 256) >= 200 && mean >= (OP == OP_WGRAD ? 512 : 128))
+  if (tiles(256, 256) >= 160 && mean >= (OP == OP_WGRAD ? 512 : 128))
     return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, true>(a, st);
-  if constexpr (MX) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
+  if constexpr (MX || OP == OP_WGRAD) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
   else return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, true>(a, st);
 }
 
