@@ -86,7 +86,7 @@ __device__ __forceinline__ int swz_col(int k) {
 
 // TY: row type; BM x BN: the tile (with the gate: BN / 2 columns of the result); WM x WN: its waves;
 // NST: stages in LDS; WIDE: MXFP4 scales of a row begin at multiples of four bytes
-template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST>
+template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool WIDE>
 struct Tile {
   static constexpr int W = WM * WN, T = 64 * W;               // waves, threads
   static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 results of a wave
@@ -97,9 +97,10 @@ struct Tile {
   static constexpr bool MCOL = OP == OP_WGRAD, NCOL = OP != OP_FORWARD, MX = TY == MOE_ROWS_MXFP4;
   static constexpr int ABYTES = BM * kKB, BBYTES = BN * kKB, STAGE = ABYTES + BBYTES;
   static constexpr int AI = ABYTES / 1024 / W, BI = BBYTES / 1024 / W;  // loads of a wave per stage
-  // MXFP4 scales: 16 bytes a row, enough for two stages; loads of a wave per two stages
+  // MXFP4 scales: 16 bytes a row at once, for two stages (PAIR) or for one of them, in as many buffers; a wave's loads
+  static constexpr bool PAIR = MX && WIDE && NST == 2;
   static constexpr int SI = MX ? ((BM + BN) / 64 + W - 1) / W : 0, SBYTES = SI * W * 1024;
-  static constexpr int LDS = NST * STAGE + 2 * SBYTES;
+  static constexpr int LDS = NST * (STAGE + SBYTES);
   static constexpr int E16 = TY == MOE_ROWS_BF16 ? 8 : TY == MOE_ROWS_INT8 ? 16 : 32;  // elements in 16 bytes
   using Acc = typename std::conditional<TY == MOE_ROWS_INT8, i32x4, f32x4>::type;
   static_assert(AI * 1024 * W == ABYTES && BI * 1024 * W == BBYTES, "whole loads");
@@ -109,7 +110,6 @@ struct Tile {
   static_assert((!MCOL || BM >= 64) && (!NCOL || BN >= 128), "swz_col stays within a row");
   static_assert(F % G == 0 && (!GATED || FN % 2 == 0), "whole groups of results");
   static_assert(!MX || BM % 64 == 0, "a load of scales is of one side");
-  static_assert(!MX || NST == 2, "scales are loaded one stage ahead of the first of their two");
 };
 
 // the n index (within the tile; for the gate: row of w relative to its half, and the half) of LDS row p of the n side:
@@ -125,7 +125,7 @@ __device__ __forceinline__ int n_of(int p, int &half) {
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
 __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 1 : 2) experts_kernel(ExpertsArgs a) {
-  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST>;
+  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST, WIDE>;
   constexpr bool MX = C::MX;
   extern __shared__ __align__(1024) char lds[];
   int *first = (int *)(lds + C::LDS);  // [E + 1] tiles along m before each expert
@@ -162,14 +162,17 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 
   // Workgroups go round the 8 XCDs, each with an L2 of its own: an XCD's workgroups take neighbouring tiles, so that
   // those that run together share operands in that L2.  Forward and dgrad: XCD x takes the x-th eighth of all tiles.
-  // wgrad, where a tile costs what its expert has rows: the x-th eighth of each expert's, if it has 64 or more.
+  // wgrad, where a tile costs what its expert has rows: an eighth of each expert's, of expert e the (x + e)-th, so that
+  // every eight experts give an XCD as many tiles as one expert has.
   const uint32_t xcd = blockIdx.x & 7, per = (gridDim.x + 7 - xcd) >> 3;  // its workgroups
   const uint32_t each = (uint32_t)wmt * (uint32_t)ntn;                    // wgrad: tiles of an expert
-  const bool split = OP == OP_WGRAD && each >= 64;
-  const uint32_t mine0 = split ? each * xcd / 8 : 0, mine = split ? each * (xcd + 1) / 8 - mine0 : each;
-  uint32_t round = 0, last = mine * (uint32_t)E;  // fits: see launch_cfg
-  if (!split) {
-    const uint64_t tiles = OP == OP_WGRAD ? last : (uint64_t)(uint32_t)first[E] * (uint32_t)ntn;
+  auto eighth = [&](uint32_t i) LAMBDA { return each * (i & 7) / 8; };    // the first tile of an eighth; each < 2^21
+  uint32_t round = 0, last;                                               // fits: see launch_cfg
+  if (OP == OP_WGRAD) {
+    last = (uint32_t)E / 8 * each;
+    for (uint32_t i = xcd; i < xcd + E % 8; ++i) last += ((i & 7) == 7 ? each : eighth(i + 1)) - eighth(i);
+  } else {
+    const uint64_t tiles = (uint64_t)(uint32_t)first[E] * (uint32_t)ntn;
     round = (uint32_t)(tiles * xcd / 8);
     last = (uint32_t)(tiles * (xcd + 1) / 8);
   }
@@ -194,15 +197,23 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
   // columns.  Byte offsets of the lane's 16 bytes, the same in all stages:
   uint32_t ao[C::AI], bo[C::BI], so[MX ? C::SI : 1];
   const char *sbase[MX ? C::SI : 1];  // MXFP4 scales: of the operand of the wave's load, and their bytes
-  int sbytes[MX ? C::SI : 1];
+  int sbytes[MX ? C::SI : 1], mshift = 0, nshift = 0;
   i32x4 mres, nres[C::HALVES];  // row operands: over the tile's rows
   auto enter = [&]() LAMBDA {
     int me;
     uint32_t rem;  // the expert's tiles along m, and which of its tiles this is
     if (OP == OP_WGRAD) {
-      e = (int)(tile / mine);
       me = wmt;
-      rem = mine0 + tile - (uint32_t)e * mine;
+      e = (int)(tile / each) * 8;
+      rem = tile - tile / each * each;  // among the eight experts' eighths: fewer than `each` tiles in all
+      for (uint32_t i = xcd;; ++i, ++e) {
+        const uint32_t from = eighth(i), n = ((i & 7) == 7 ? each : eighth(i + 1)) - from;
+        if (rem < n) {
+          rem += from;
+          break;
+        }
+        rem -= n;
+      }
     } else {
       // the last expert whose tiles begin at or before mg (it has some): 64 experts compared at once
       const uint32_t mg = tile / (uint32_t)ntn;
@@ -259,18 +270,26 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
       for (int i = 0; i < C::SI; ++i) {  // LDS rows of scales: the m side's, then the n side's
         const int p = (wave * C::SI + i) * 64 + lane;
         const bool mside = (wave * C::SI + i) * 64 < BM;
-        sbase[i] = mside ? (const char *)a.ms + (lo + m0) * sw : (const char *)a.ns + ((int64_t)e * nw + n0) * sw;
-        const int64_t bytes = (int64_t)(mside ? cnt - m0 : nw - n0) * sw;
-        sbytes[i] = (int)(bytes < 0x7fffffff ? bytes : 0x7fffffff);
+        const char *from = mside ? (const char *)a.ms + (lo + m0) * sw : (const char *)a.ns + ((int64_t)e * nw + n0) * sw;
+        // whole words: up to three bytes before the first row's and behind the last's are read with theirs
+        const int off = WIDE ? 0 : (int)((uintptr_t)from & 3);
+        sbase[i] = from - off;
+        const int64_t bytes = ((int64_t)(mside ? cnt - m0 : nw - n0) * sw + off + 3) & ~(int64_t)3;
+        sbytes[i] = (int)(bytes < 0x7ffffff0 ? bytes : 0x7ffffff0);
         if (p < BM) {
-          so[i] = m0 + p < cnt ? (uint32_t)(p * sw) : kOut;
+          so[i] = m0 + p < cnt ? (uint32_t)(p * sw + off) & ~3u : kOut;
         } else if (p < BM + BN) {
           int half;
           const int n = n_of<C>(p - BM, half);
-          so[i] = n0 + n < a.N ? (uint32_t)((n + (GATED && half ? a.N : 0)) * sw) : kOut;
+          so[i] = n0 + n < a.N ? (uint32_t)((n + (GATED && half ? a.N : 0)) * sw + off) & ~3u : kOut;
         } else {
           so[i] = kOut;
         }
+      }
+      if constexpr (!WIDE) {  // where in its 16 bytes the lane's row begins: the rows of a lane differ by multiples of four
+        const int r = lane & 15;
+        mshift = (int)((uintptr_t)a.ms + (lo + m0) * sw + r * sw) & 3;
+        nshift = (int)((uintptr_t)a.ns + ((int64_t)e * nw + n0) * sw + r * sw) & 3;
       }
     }
   };
@@ -295,22 +314,17 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
                   mside ? mlds : nlds, more);
     }
   };
-  // the scales of stages 2 t and 2 t + 1, 16 bytes a row (the last piece may run on into the next row's: see
-  // scales), into the other of their two buffers
+  // MXFP4 scales, 16 bytes a row at once.  PAIR: of stages 2 u and 2 u + 1, into the other of the two buffers.
+  // Otherwise of stage u into buffer b, 8 bytes and what lies around them: rows of scales that begin at any byte
+  // (not WIDE) are read from the multiple of four before.  Either way pieces may run on into the next row's
+  // scales: see scale_pair.
   int sbuf = 1;
-  auto issue_scales = [&](int t) LAMBDA {
+  auto issue_scales = [&](int u, int b) LAMBDA {
 #pragma unroll
     for (int i = 0; i < C::SI; ++i) {
-      const uint32_t at = lds0 + NST * C::STAGE + (sbuf ^ 1) * C::SBYTES + (wave * C::SI + i) * 1024;
-      if constexpr (WIDE) {
-        load_to_lds(resource(sbase[i] + t * 16, t * 16 < sw ? sbytes[i] - t * 16 : 0), so[i], 0, at, 0);
-      } else {  // a byte at a time through registers; zeros behind the rows' end
-        u32x4 v = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (so[i] != kOut && t * 16 + q < sw) v[q / 4] |= (uint32_t)(uint8_t)sbase[i][(int64_t)so[i] + t * 16 + q] << (q % 4 * 8);
-        *(__attribute__((address_space(3))) u32x4 *)(uintptr_t)(at + lane * 16) = v;
-      }
+      const int from = u * (C::PAIR ? 16 : 8), to = C::PAIR ? sbuf ^ 1 : b;
+      load_to_lds(resource(sbase[i] + from, from < sw ? sbytes[i] - from : 0), so[i], 0,
+                  lds0 + NST * C::STAGE + to * C::SBYTES + (wave * C::SI + i) * 1024, 0);
     }
   };
 
@@ -353,13 +367,18 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
   // MXFP4: the scale bytes of the lane's two pieces of stage s (even: b = 0), of two rows in one register
   constexpr int SM = MX ? (C::FM + 1) / 2 : 1, SN = MX ? (C::FN + 1) / 2 : 1;
   uint32_t sa[SM], sb[SN];
-  auto scale_pair = [&](uint32_t p, int s, int b, int i, int n) LAMBDA -> uint32_t {
-    typedef __attribute__((address_space(3))) const uint16_t *lds_u16;
-    const uint32_t at = p + sbuf * C::SBYTES + b * 8 + i * 512;
-    uint32_t v = *(lds_u16)(uintptr_t)at;
-    if (2 * i + 1 < n) v |= (uint32_t) * (lds_u16)(uintptr_t)(at + 256) << 16;
-    // blocks behind the rows' end: not the next rows' scales, which may be NaN (sw is a multiple of 4)
-    return !WIDE || s * 8 + g * 2 < sw ? v : 0;
+  auto scale_pair = [&](uint32_t p, int s, int b, int i, int n, int shift) LAMBDA -> uint32_t {
+    typedef uint16_t __attribute__((aligned(1))) u16_any;
+    auto two = [](uint32_t x) LAMBDA -> uint32_t {
+      if constexpr (WIDE) return *(__attribute__((address_space(3))) const uint16_t *)(uintptr_t)x;
+      else return *(__attribute__((address_space(3))) const u16_any *)(uintptr_t)x;
+    };
+    const uint32_t at = p + (C::PAIR ? sbuf * C::SBYTES + b * 8 : b * C::SBYTES + shift) + i * 512;
+    uint32_t v = two(at);
+    if (2 * i + 1 < n) v |= two(at + 256) << 16;
+    // blocks behind the rows' end: not the next rows' scales, which may be NaN (WIDE: sw is a multiple of 4)
+    const int left = sw - s * 8 - g * 2;
+    return left >= 2 ? v : !WIDE && left == 1 ? v & 0xff00ffu : 0;
   };
 
   typename C::Acc acc[C::FM][C::FN];
@@ -385,18 +404,23 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 
   // ---- a stage, in buffer b of the ring.  The products of one step of 64 bytes of k run while the next step's
   // operands come from LDS.  Before those are the next stage's, every wave has read this stage, so its buffer
-  // takes the loads of stage `ahead`, and the next stage's loads have to be there.  after: the next stage.  A wave
+  // takes the loads of stage `ahead`, and the next stage's loads have to be there.  after: the next stage (its scales'
+  // shifts: msh, nsh).  A wave
   // without rows (IDLE) only loads and waits.
-  auto stage = [&](auto b_, auto idle_, int after, int ahead) LAMBDA {
+  auto stage = [&](auto b_, auto idle_, int after, int ahead, int msh, int nsh) LAMBDA {
     constexpr int b = decltype(b_)::value, bn = (b + 1) % NST;
     constexpr bool IDLE = decltype(idle_)::value;
     static_for<2>([&](auto ks_) LAMBDA {
       constexpr int ks = decltype(ks_)::value;
       if constexpr (ks == 1) {
-        stage_wait<(NST - 2) * LOADS>();
+        stage_wait<(NST - 2) * (LOADS + (C::PAIR ? 0 : C::SI))>();
         if constexpr (MX) {
-          if (b == 1) sbuf ^= 1;
-          if (b == 0) issue_scales(ahead / 2);
+          if constexpr (!C::PAIR) {
+            issue_scales(ahead, b);
+          } else {
+            if (b == 1) sbuf ^= 1;
+            if (b == 0) issue_scales(ahead / 2, 0);
+          }
         }
       }
       static_for<C::FM>([&](auto i_) LAMBDA {
@@ -411,10 +435,10 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
         for (int j = i * C::FN / C::FM; j < (i + 1) * C::FN / C::FM; ++j) fb[ks ^ 1][j] = read_n(ks == 1 ? bn : b, j, ks ^ 1);
         fa[ks ^ 1][i] = read_m(ks == 1 ? bn : b, i, ks ^ 1);
         if constexpr (MX && ks == 1) {  // the next stage's scales, where this one's are done with
-          if constexpr (i % 2 == 1 || i == C::FM - 1) sa[i / 2] = scale_pair(sm, after, bn, i / 2, C::FM);
+          if constexpr (i % 2 == 1 || i == C::FM - 1) sa[i / 2] = scale_pair(sm, after, bn, i / 2, C::FM, msh);
           if constexpr (i == C::FM - 1) {
 #pragma unroll
-            for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, after, bn, j, C::FN);
+            for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, after, bn, j, C::FN, nsh);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -424,17 +448,20 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 
   auto fill = [&]() LAMBDA {
     sbuf = 1;
-    if constexpr (MX) issue_scales(0);
+    if constexpr (C::PAIR) issue_scales(0, 0);
     sbuf = 0;
-    static_for<NST>([&](auto b_) LAMBDA { static_for<LOADS>([&](auto l_) LAMBDA { issue(decltype(b_)::value, b_, l_); }); });
+    static_for<NST>([&](auto b_) LAMBDA {
+      if constexpr (MX && !C::PAIR) issue_scales(decltype(b_)::value, decltype(b_)::value);
+      static_for<LOADS>([&](auto l_) LAMBDA { issue(decltype(b_)::value, b_, l_); });
+    });
   };
   auto begin = [&]() LAMBDA {
-    stage_wait<(NST - 1) * LOADS>();
+    stage_wait<(NST - 1) * (LOADS + (C::PAIR ? 0 : C::SI))>();
     if constexpr (MX) {
 #pragma unroll
-      for (int i = 0; i < SM; ++i) sa[i] = scale_pair(sm, 0, 0, i, C::FM);
+      for (int i = 0; i < SM; ++i) sa[i] = scale_pair(sm, 0, 0, i, C::FM, mshift);
 #pragma unroll
-      for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, 0, 0, j, C::FN);
+      for (int j = 0; j < SN; ++j) sb[j] = scale_pair(sn, 0, 0, j, C::FN, nshift);
     }
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) fb[0][j] = read_n(0, j, 0);
@@ -455,13 +482,16 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
     const int turns = stages > NST ? (stages + NST - 1) / NST : 1, full = RING ? turns - 1 : turns;
     auto run = [&](auto idle_) LAMBDA {
       for (int s0 = 0; s0 < full * NST; s0 += NST)
-        static_for<NST>([&](auto b_) LAMBDA { stage(b_, idle_, s0 + decltype(b_)::value + 1, s0 + decltype(b_)::value + NST); });
+        static_for<NST>([&](auto b_) LAMBDA {
+          stage(b_, idle_, s0 + decltype(b_)::value + 1, s0 + decltype(b_)::value + NST, mshift, nshift);
+        });
     };
     // a tile that ends before the wave's rows (in RING's last turn the products of such a wave are of no use)
     if (WM > 1 && m0 + mfirst >= (OP == OP_WGRAD ? a.M : cnt)) run(std::true_type{});
     else run(std::false_type{});
     const int m1 = m0, n1 = n0, e1 = e, mlim = OP == OP_WGRAD ? a.M : cnt;  // mlim: rows of the result
     const int64_t lo1 = lo;
+    [[maybe_unused]] const int ms1 = mshift, ns1 = nshift;
     round += per;
     place += kTurn % per;
     if (place >= per) place -= per;
@@ -470,7 +500,8 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
       if (tile < last) enter();  // else this one's again, for nothing
       static_for<NST>([&](auto b_) LAMBDA {
         constexpr int b = decltype(b_)::value;
-        stage(b_, std::false_type{}, b + 1 < NST ? (turns - 1) * NST + b + 1 : 0, b);
+        constexpr bool same = b + 1 < NST;  // the next stage is this tile's
+        stage(b_, std::false_type{}, same ? (turns - 1) * NST + b + 1 : 0, b, same ? ms1 : mshift, same ? ns1 : nshift);
       });
     } else {  // the next tile's first loads go out before this one's results
       stage_wait<0>();
@@ -530,7 +561,7 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
 static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
-  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST>;
+  using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST, WIDE>;
   // at most (2^27 / 64 + 2^11) * 2^10 or 2^21 * 2^10 tiles: below 2^32
   const int64_t mt = OP == OP_WGRAD ? (int64_t)a.g.E * ((a.M + BM - 1) / BM) : a.g.rows / BM + a.g.E;
   const int64_t tiles = mt * ((a.N + C::CO - 1) / C::CO);
@@ -541,59 +572,80 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
   hipLaunchKernelGGL(k, dim3(grid), dim3(C::T), lds, st, a);
   return hipGetLastError();
 }
-// The tile.  Figures: us on one MI355X, every operand from HBM.
-//  16 x 64, 2 waves, four stages       forward with at most 16 rows an expert: weights streamed once, three workgroups
-//                      a CU.  8 rows of 8 experts, 4096 -> 2 x 1024 bf16: 22; 64 x 128: 23, 128 x 128: 28
-//  64 x 128, 4 waves, four stages      at most 64 rows an expert
-//  128 x 128, 4 waves, four stages     hardly more tiles than CUs: depth counts.  13 x 235 rows, dgrad 2056 -> 1048: 29
-//                      against 38 with two stages and two workgroups a CU, 59 with 256 x 256
-//  256 x 256, 8 waves, two stages      tiles for most CUs and long sums: 16 x 2048 rows, 4096 -> 4096 bf16: 881; 128 x
-//                      128: 1175, 128 x 256: 1200
-//  256 x 128, 8 waves, three stages    between them: the rows of an expert in one tile, its waves without rows idle.
-//                      1024 rows on 8 experts, 7168 -> 2 x 2048 int8: 58; 128 x 128: 76, 256 x 256: 92
-//  128 x 128, two stages, two workgroups a CU     the same for wgrad (13 x 235 rows: 35 against 41) and for MXFP4,
-//                      which has two stages always (see Tile)
-template <int TY, int OP, bool GATED, bool F32>
+// The tile: 16 x 64 for forward with at most 16 rows an expert (weights streamed once, three workgroups a CU: 8 rows of
+// 8 experts, 4096 -> 2 x 1024 bf16 in 22 us; 64 x 128: 23, 128 x 128: 28), 64 x 128 for at most 64; else what comes
+// out fastest by rounds of tiles over the CUs x (stages x time of a stage + time between tiles), measured in us
+// on one MI355X where the tiles fill the chip:
+//                                               stage  between   16 x 2048 rows, 4096 -> 4096 bf16
+//   256 x 256, 8 waves, two stages, one a CU     1.72     4      870 us
+//   256 x 128, 8 waves, three stages, one a CU   0.93     2.5    957   (an expert's few rows in one tile, its waves
+//                                                                      without rows idle)
+//   128 x 128, 4 waves, two stages, two a CU     1.15     1.5    1175
+//   128 x 128, 4 waves, four stages, one a CU    0.60     2      1173  (deep: for hardly more tiles than CUs)
+// Within 15 % of what was measured on 1024 to 32768 rows of 4 to 64 experts.  The second would need three stages of
+// scales too and is not there for MXFP4, nor the first for scales at odd addresses (not WIDE), which fill its
+// registers.  In wgrad a tile costs what its expert has rows: the largest is
+// taken to have three times the mean.
+template <int TY, int OP, bool GATED, bool F32, bool WIDE>
 static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
   constexpr bool MX = TY == MOE_ROWS_MXFP4;
-  constexpr int DEEP = MX ? 2 : 4;
+  constexpr int E16 = TY == MOE_ROWS_BF16 ? 8 : TY == MOE_ROWS_INT8 ? 16 : 32;
   const int64_t E = a.g.E, mean = (a.g.rows + E - 1) / E, m = OP == OP_WGRAD ? a.M : mean;
-  // tiles to expect: ragged rows leave half a tile an expert empty
   auto tiles = [&](int bm, int bn) {
-    if (GATED) bn /= 2;
-    return (OP == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm) * ((a.N + bn - 1) / bn);
+    const int64_t co = GATED ? bn / 2 : bn;
+    // ragged rows leave half a tile an expert empty
+    const int64_t mt = OP == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm;
+    return mt * ((a.N + co - 1) / co);
   };
-  if constexpr (MX) {
-    // rows of scales that do not begin at multiples of four bytes are copied byte by byte
-    if (a.K % 128 != 0 || (((uintptr_t)a.ms | (uintptr_t)a.ns) & 3) != 0)
-      return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, false>(a, st);
-  }
   if constexpr (OP == OP_FORWARD && !MX) {
     if (mean <= 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);
   }
-  if (m <= 64) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, DEEP, true, true>(a, st);
-  if constexpr (!MX) {
-    if (tiles(128, 128) <= 256) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, true>(a, st);
+  if (m <= 64) {
+    if (MX && tiles(64, 128) > 256) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 2, true, WIDE>(a, st);
+    return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 4, true, WIDE>(a, st);
   }
-  if (tiles(256, 256) >= 160 && mean >= (OP == OP_WGRAD ? 512 : 128))
-    return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, true>(a, st);
-  if constexpr (MX || OP == OP_WGRAD) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, true>(a, st);
-  else return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, true>(a, st);
+  const double stages = OP == OP_FORWARD ? (a.K / E16 + 7) / 8 : OP == OP_DGRAD ? (a.K + 63) / 64 : (mean + 63) / 64;
+  auto time = [&](int bm, int bn, int slots, double stage, double between) {
+    const double rounds = (double)((tiles(bm, bn) + slots - 1) / slots), one = stages * stage + between;
+    const double largest = OP == OP_WGRAD ? (E < 3 ? E : 3) * stages * stage : 0.0;
+    return rounds * one > largest ? rounds * one : largest;
+  };
+  const double big = time(256, 256, 256, 1.72, 4.0), two = time(128, 128, 512, 1.15, 1.5);
+  const double wide = time(256, 128, 256, 0.93, 2.5), deep = time(128, 128, 256, 0.60, 2.0);
+  if constexpr (MX) {
+    if constexpr (WIDE) {
+      if (big <= two && big <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
+    }
+  } else {
+    if (big <= two && big <= wide && big <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
+    if (wide <= two && wide <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, WIDE>(a, st);
+  }
+  if (deep <= two) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, WIDE>(a, st);
+  return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, WIDE>(a, st);
+}
+
+// MXFP4: whether every row of scales begins at a multiple of four bytes
+template <int TY, int OP, bool GATED, bool F32>
+static hipError_t launch_type(const ExpertsArgs &a, hipStream_t st) {
+  if constexpr (TY == MOE_ROWS_MXFP4) {
+    if (a.K % 128 != 0 || (((uintptr_t)a.ms | (uintptr_t)a.ns) & 3) != 0) return launch_tile<TY, OP, GATED, F32, false>(a, st);
+  }
+  return launch_tile<TY, OP, GATED, F32, true>(a, st);
 }
 
 hipError_t launch_experts(const ExpertsArgs &a, int op, int row_type, int act, bool out_fp32, hipStream_t st) {
   if (op != OP_WGRAD && a.g.rows == 0) return hipSuccess;
-  if (op == OP_DGRAD) return launch_tile<MOE_ROWS_BF16, OP_DGRAD, false, false>(a, st);
+  if (op == OP_DGRAD) return launch_type<MOE_ROWS_BF16, OP_DGRAD, false, false>(a, st);
   if (op == OP_WGRAD)
-    return out_fp32 ? launch_tile<MOE_ROWS_BF16, OP_WGRAD, false, true>(a, st)
-                    : launch_tile<MOE_ROWS_BF16, OP_WGRAD, false, false>(a, st);
+    return out_fp32 ? launch_type<MOE_ROWS_BF16, OP_WGRAD, false, true>(a, st)
+                    : launch_type<MOE_ROWS_BF16, OP_WGRAD, false, false>(a, st);
   if (act == MOE_ACT_SWIGLU)
-    return row_type == MOE_ROWS_BF16   ? launch_tile<MOE_ROWS_BF16, OP_FORWARD, true, false>(a, st)
-           : row_type == MOE_ROWS_INT8 ? launch_tile<MOE_ROWS_INT8, OP_FORWARD, true, false>(a, st)
-                                       : launch_tile<MOE_ROWS_MXFP4, OP_FORWARD, true, false>(a, st);
-  return row_type == MOE_ROWS_BF16   ? launch_tile<MOE_ROWS_BF16, OP_FORWARD, false, false>(a, st)
-         : row_type == MOE_ROWS_INT8 ? launch_tile<MOE_ROWS_INT8, OP_FORWARD, false, false>(a, st)
-                                     : launch_tile<MOE_ROWS_MXFP4, OP_FORWARD, false, false>(a, st);
+    return row_type == MOE_ROWS_BF16   ? launch_type<MOE_ROWS_BF16, OP_FORWARD, true, false>(a, st)
+           : row_type == MOE_ROWS_INT8 ? launch_type<MOE_ROWS_INT8, OP_FORWARD, true, false>(a, st)
+                                       : launch_type<MOE_ROWS_MXFP4, OP_FORWARD, true, false>(a, st);
+  return row_type == MOE_ROWS_BF16   ? launch_type<MOE_ROWS_BF16, OP_FORWARD, false, false>(a, st)
+         : row_type == MOE_ROWS_INT8 ? launch_type<MOE_ROWS_INT8, OP_FORWARD, false, false>(a, st)
+                                     : launch_type<MOE_ROWS_MXFP4, OP_FORWARD, false, false>(a, st);
 }
 
 }  // namespace moe
