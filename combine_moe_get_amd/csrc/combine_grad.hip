@@ -6,7 +6,9 @@
 //   constant slot   grad of x: += w alpha1 g; of w: <g, alpha1 x + alpha2 v>;
 //                   alpha1 += w g x, alpha2 += w g v, v += w g alpha2 (all element-wise, over all tokens)
 //   zero, dropped or masked slot: nothing; w: 0
-// One workgroup a token: g is read once, every expert row once and every gradient row is written once.
+// One workgroup a token: g is read once, every expert row once and every gradient row is written once, so memory
+// bounds it: 4096 tokens of 4096 with 8 of 64 experts (576 MB) 95 us, 6.1 TB/s; 128 tokens of 7168 (31 MB, mostly
+// from the caches) 11 us; with copy and constant experts see below.
 // The gradients of the constant experts' vectors are sums over tokens: a second kernel, one workgroup per
 // (expert, 64 columns), whose waves each take every sixteenth part of the slots in order and are added in
 // order, so that the result does not depend on the launch.
@@ -30,10 +32,12 @@ __device__ __forceinline__ void unpack8g(const u32x4 &v, float *f) {
 
 enum : int { G_NONE = 0, G_ROUTED = 1, G_COPY = 2, G_CONST = 3 };
 
-// One workgroup a token, a thread U chunks of 8 elements; threads past the row's end only take part in the sums.
-// The slots' kinds, rows and weights are wave-uniform; every row of a chunk is requested before the first is used.
-// SPECIAL: copy and constant experts can occur.
-template <int KMAX, int U, bool SPECIAL>
+// One workgroup a token, a thread one chunk of 8 elements (two a thread, in turn: 99 us for the 95 above, 8.4 for 6.7
+// on 16 tokens of 7168); threads past the row's end only take part in the sums.  The slots' kinds, rows and weights are
+// wave-uniform; every row is requested before the first is used.  KMAX: the least of 1, 2, 4, 8, 16 that holds the
+// slots (K = 8 with 16: 12.5 us for 128 tokens of 7168, 10.7 with 8).  SPECIAL: copy and constant experts can occur;
+// without them there is no x to read.
+template <int KMAX, bool SPECIAL>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;
   __shared__ float part[16][KMAX];
@@ -48,15 +52,11 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
     wt = c.w[(size_t)t * K + lane];
     r = c.dst_row[(size_t)t * K + lane];
   }
-  u32x4 gv[U], xv[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int ch = tid + u * blockDim.x;
-    gv[u] = xv[u] = u32x4{0u, 0u, 0u, 0u};
-    if (ch < nch) {
-      gv[u] = ((const u32x4 *)(a.go + (size_t)t * H))[ch];
-      if (SPECIAL) xv[u] = ((const u32x4 *)(c.ori_x + (size_t)t * H))[ch];
-    }
+  const bool in = tid < nch;
+  u32x4 gv = {0u, 0u, 0u, 0u}, xv = {0u, 0u, 0u, 0u};
+  if (in) {
+    gv = ((const u32x4 *)(a.go + (size_t)t * H))[tid];
+    if (SPECIAL) xv = ((const u32x4 *)(c.ori_x + (size_t)t * H))[tid];
   }
   int k = G_NONE;
   if (live && lane < K) {
@@ -79,65 +79,60 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
     w[j] = readlane_f(wt, j);
     dot[j] = 0.0f;
   }
+  u32x4 yv[KMAX];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int ch = tid + u * blockDim.x;
-    const bool in = ch < nch;
-    u32x4 yv[KMAX];
+  for (int j = 0; j < KMAX; ++j) {
+    yv[j] = u32x4{0u, 0u, 0u, 0u};
+    if (kind[j] == G_ROUTED && a.gw && in) yv[j] = __builtin_nontemporal_load((const u32x4 *)c.y + (size_t)row[j] * nch + tid);
+  }
+  float g[8], x[8], gx[8];
+  unpack8g(gv, g);
+  unpack8g(xv, x);
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      yv[j] = u32x4{0u, 0u, 0u, 0u};
-      if (kind[j] == G_ROUTED && a.gw && in) yv[j] = __builtin_nontemporal_load((const u32x4 *)c.y + (size_t)row[j] * nch + ch);
-    }
-    float g[8], x[8], gx[8];
-    unpack8g(gv[u], g);
-    unpack8g(xv[u], x);
+  for (int e = 0; e < 8; ++e) gx[e] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gx[e] = 0.0f;
+  for (int j = 0; j < KMAX; ++j) {
+    if (kind[j] == G_NONE) continue;
+    float y[8];
+    if (!SPECIAL || kind[j] == G_ROUTED) {
+      unpack8g(yv[j], y);
+      if (a.gy && in) {
+        u32x4 o;
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      if (kind[j] == G_NONE) continue;
-      float y[8];
-      if (!SPECIAL || kind[j] == G_ROUTED) {
-        unpack8g(yv[j], y);
-        if (a.gy && in) {
-          u32x4 o;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = pack2g(w[j] * g[2 * e], w[j] * g[2 * e + 1]);
-          __builtin_nontemporal_store(o, (u32x4 *)a.gy + (size_t)row[j] * nch + ch);
-        }
-      } else if (kind[j] == G_COPY) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = x[e];
-          gx[e] = __builtin_fmaf(w[j], g[e], gx[e]);
-        }
-      } else {
-        float a1[8], a2[8], v[8];
-        const size_t at = (size_t)row[j] * nch + (in ? ch : 0);  // threads past the end: g = 0
-        unpack8g(((const u32x4 *)c.a1)[at], a1);
-        unpack8g(((const u32x4 *)c.a2)[at], a2);
-        unpack8g(((const u32x4 *)c.cv)[at], v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = __builtin_fmaf(a1[e], x[e], a2[e] * v[e]);
-          gx[e] = __builtin_fmaf(w[j] * a1[e], g[e], gx[e]);
-        }
+        for (int e = 0; e < 4; ++e) o[e] = pack2g(w[j] * g[2 * e], w[j] * g[2 * e + 1]);
+        __builtin_nontemporal_store(o, (u32x4 *)a.gy + (size_t)row[j] * nch + tid);
       }
-      if (a.gw && in) {
+    } else if (kind[j] == G_COPY) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(g[e], y[e], dot[j]);
+      for (int e = 0; e < 8; ++e) {
+        y[e] = x[e];
+        gx[e] = __builtin_fmaf(w[j], g[e], gx[e]);
+      }
+    } else {
+      float a1[8], a2[8], v[8];
+      const size_t at = (size_t)row[j] * nch + (in ? tid : 0);  // threads past the end: g = 0
+      unpack8g(((const u32x4 *)c.a1)[at], a1);
+      unpack8g(((const u32x4 *)c.a2)[at], a2);
+      unpack8g(((const u32x4 *)c.cv)[at], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = __builtin_fmaf(a1[e], x[e], a2[e] * v[e]);
+        gx[e] = __builtin_fmaf(w[j] * a1[e], g[e], gx[e]);
       }
     }
-    if (SPECIAL && a.gx && in) {
-      u32x4 o;
+    if (a.gw && in) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = pack2g(gx[2 * e], gx[2 * e + 1]);
-      __builtin_nontemporal_store(o, (u32x4 *)(a.gx + (size_t)t * H) + ch);
+      for (int e = 0; e < 8; ++e) dot[j] = __builtin_fmaf(g[e], y[e], dot[j]);
     }
   }
+  if (SPECIAL && a.gx && in) {
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack2g(gx[2 * e], gx[2 * e + 1]);
+    __builtin_nontemporal_store(o, (u32x4 *)(a.gx + (size_t)t * H) + tid);
+  }
   if (!SPECIAL && a.gx) {  // no copy and no constant experts: zeros
-    for (int ch = tid; ch < nch; ch += blockDim.x) ((u32x4 *)(a.gx + (size_t)t * H))[ch] = u32x4{0u, 0u, 0u, 0u};
+    if (in) ((u32x4 *)(a.gx + (size_t)t * H))[tid] = u32x4{0u, 0u, 0u, 0u};
   }
   if (a.gw) {
 #pragma unroll
@@ -157,7 +152,8 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
 
 // workgroup (64 columns, constant expert): 16 waves, wave v adds the slots of the v-th sixteenth of the tokens, in
 // order.  A wave looks at 512 slots at a time (eight loads under way), lists the ones it is looking for in LDS and
-// takes eight of them at a time.
+// takes eight of them at a time.  4096 x 8 slots on 64 + 8 experts, 4 constant ones of 4096: 22 us, by which order the
+// sums and not memory bound it; the tokens' gradients with it: 107 us.
 constexpr int kScan = 512, kTake = 8;
 __global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;
@@ -224,18 +220,12 @@ __global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
   }
 }
 
-template <int KMAX, int U>
-static void launch_u(const CombineGradArgs &a, hipStream_t st) {
-  const int nch = a.c.H >> 3;
-  const dim3 grid((unsigned)a.c.T), block((unsigned)((nch + 64 * U - 1) / (64 * U) * 64));  // nch <= 1024
-  if (a.c.C + a.c.Kc > 0) hipLaunchKernelGGL((combine_grad_kernel<KMAX, U, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((combine_grad_kernel<KMAX, U, false>), grid, block, 0, st, a);
-}
-
 template <int KMAX>
 static void launch_k(const CombineGradArgs &a, hipStream_t st) {
-  if (a.c.T <= 512) launch_u<KMAX, 1>(a, st);  // few workgroups: more threads in each
-  else launch_u<KMAX, 2>(a, st);
+  const int nch = a.c.H >> 3;
+  const dim3 grid((unsigned)a.c.T), block((unsigned)((nch + 63) / 64 * 64));  // nch <= 1024
+  if (a.c.C + a.c.Kc > 0) hipLaunchKernelGGL((combine_grad_kernel<KMAX, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((combine_grad_kernel<KMAX, false>), grid, block, 0, st, a);
 }
 
 hipError_t launch_combine_grad(const CombineGradArgs &a, hipStream_t st) {

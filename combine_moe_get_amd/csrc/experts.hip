@@ -9,6 +9,14 @@
 // pieces; one whose k runs across memory ("column" operand: 64 rows of k per stage, bf16 only) is read
 // with the transposing LDS load.  The matrix instructions of all types take 64 bytes of k per row and
 // 16 bytes per lane, so one kernel serves them.
+//
+// A workgroup is persistent: it keeps a ring of stages in LDS filled by loads that go past the registers, and multiplies
+// one stage's operands while the next one's come from LDS, on to the next tile without a pause where the ring allows it.
+// Bounds: few rows an expert, the weights from memory (8 rows of 8 experts, 134 MB: 25 us, 5.4 TB/s; 16 of 32 in 4 bits,
+// 883 MB with their scales: 157 us, 5.6 TB/s).  Many rows: a stage of a 256 x 256 tile is 2048 cycles of matrix
+// instructions on each SIMD and 2048 of LDS (64 KB in, 192 KB out, 128 bytes a cycle), which do not overlap wholly: 1.72
+// us, at the 1.95 GHz of such a load 3350.  16 x 2048 rows of 4096 -> 4096 870 us, 1.26 PFLOP/s (torch's plain product
+// of 8192: 1.37, of 16384: 1.61); int8 2.6 POP/s, 4 bits 4 PFLOP/s.
 #include "experts_internal.hpp"
 
 namespace moe {
@@ -562,7 +570,8 @@ __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
 static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
   using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST, WIDE>;
-  // at most (2^27 / 64 + 2^11) * 2^10 or 2^21 * 2^10 tiles: below 2^32
+  // Tiles fit 32 bits: 16 rows high only for at most 16 * 2^11 rows, 64 for at most 64 * 2^11, else 128 and more, so at
+  // most (2^27 / 128 + 2^11) * 2^10; wgrad: 2^11 experts of at most 2^9 * 2^9
   const int64_t mt = OP == OP_WGRAD ? (int64_t)a.g.E * ((a.M + BM - 1) / BM) : a.g.rows / BM + a.g.E;
   const int64_t tiles = mt * ((a.N + C::CO - 1) / C::CO);
   const size_t lds = C::LDS + (size_t)(a.g.E + 1) * 4;
@@ -582,10 +591,14 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
 //                                                                      without rows idle)
 //   128 x 128, 4 waves, two stages, two a CU     1.15     1.5    1175
 //   128 x 128, 4 waves, four stages, one a CU    0.60     2      1173  (deep: for hardly more tiles than CUs)
-// Within 15 % of what was measured on 1024 to 32768 rows of 4 to 64 experts.  The second would need three stages of
-// scales too and is not there for MXFP4, nor the first for scales at odd addresses (not WIDE), which fill its
-// registers.  In wgrad a tile costs what its expert has rows: the largest is
-// taken to have three times the mean.
+// The order that it gives is that of the measured times within 15 % on 1024 to 32768 rows of 4 to 64 experts (128 rows
+// of each of 4, 4096 -> 2 x 2048 bf16, in the table's order: 79, 45, 57, 41 us; 200 of 32, 2048 -> 1024: 62, 46, 50,
+// 49).  In wgrad a tile costs what its expert has rows: the largest is taken to have three times the mean.
+//   MXFP4 has the first and the third.  A stage's scales are a load more where they are read stage by stage, which three
+// and four stages would need: the fourth took 36 us against 32 for the third on 128 rows of 4 experts, 4128 -> 2 x 2048.
+// The first, with scales at odd addresses (not WIDE), runs out of registers.  64 x 128 with two stages: 16 rows of 32
+// experts, 4096 -> 2 x 4096 in 98 us (four: 110); with four for at most 256 tiles: 8 of 8, 4096 -> 2 x 1024 in 11.8 us
+// (13.5).  Scales at odd addresses cost 106 us where these cost 98.
 template <int TY, int OP, bool GATED, bool F32, bool WIDE>
 static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
   constexpr bool MX = TY == MOE_ROWS_MXFP4;
@@ -611,16 +624,16 @@ static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
     return rounds * one > largest ? rounds * one : largest;
   };
   const double big = time(256, 256, 256, 1.72, 4.0), two = time(128, 128, 512, 1.15, 1.5);
-  const double wide = time(256, 128, 256, 0.93, 2.5), deep = time(128, 128, 256, 0.60, 2.0);
   if constexpr (MX) {
     if constexpr (WIDE) {
-      if (big <= two && big <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
+      if (big <= two) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
     }
   } else {
+    const double wide = time(256, 128, 256, 0.93, 2.5), deep = time(128, 128, 256, 0.60, 2.0);
     if (big <= two && big <= wide && big <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
     if (wide <= two && wide <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, WIDE>(a, st);
+    if (deep <= two) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, WIDE>(a, st);
   }
-  if (deep <= two) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, WIDE>(a, st);
   return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, WIDE>(a, st);
 }
 

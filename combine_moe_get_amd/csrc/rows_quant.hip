@@ -33,7 +33,7 @@ __device__ __forceinline__ uint32_t e2m1(float v) {
 
 // int8.  A row is held in registers between the search for its amax and the rounding: 64 W threads a row, NC
 // chunks of 8 elements a thread; four rows (W = 1) or one (W = 4) a workgroup.  NC = 0: the row is read twice.
-// 6168 rows of 2064: see launch_rows_quant.
+// 6168 rows of 2064 in 10 us (3.8 TB/s), 8192 of 7168 in 33 us (5.3).
 template <int W, int NC>
 __global__ void __launch_bounds__(256) quant_int8_kernel(RowsQuantArgs a) {
   __shared__ float red[2][16];
@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t mx_codes(const u32x4 &v, uint32_t &s) {
 }
 
 // MXFP4: a thread takes 16 bytes, 8 elements, so that a wave reads 1 KB and writes 256 bytes at once; four loads
-// under way a thread.  32768 rows of 4096: see launch_rows_quant.
+// under way a thread.  32768 rows of 4096 in 68 to 72 us (4.7 to 5.0 TB/s; a large copy reaches 4.9).
 constexpr int kMxLoads = 4;
 __global__ void __launch_bounds__(256) quant_mxfp4_kernel(RowsQuantArgs a) {
   const int64_t n = a.rows * (a.H >> 3), step = (int64_t)gridDim.x * 256 * kMxLoads;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) quant_mxfp4_kernel(RowsQuantArgs a) {
   }
 }
 
-// the same for the rows of experts: a workgroup a row
+// the same for the rows of experts, of which some are not to be touched: a workgroup a row (taken for all rows: 76 us)
 __global__ void __launch_bounds__(256) quant_mxfp4_rows_kernel(RowsQuantArgs a) {
   const int nch = a.H >> 3;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -154,6 +154,8 @@ static void launch_int8(const RowsQuantArgs &a, hipStream_t st) {
 hipError_t launch_rows_quant(const RowsQuantArgs &a, int row_type, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
   if (row_type == MOE_ROWS_INT8) {
+    // 8192 rows, us, by <W, NC>: of 1024 6.8 <1, 2>, 8.0 <1, 8>, 12.3 <4, 4>; of 4096 18.0 <1, 8>, 18.2 <4, 4>,
+    // 20.2 <4, 0>; of 7168 33.4 <4, 4>, 39.7 <4, 0>; of 16384 103 <4, 0>, 125 <1, 0>
     if (a.H <= 1024) launch_int8<1, 2>(a, st);
     else if (a.H <= 4096) launch_int8<1, 8>(a, st);
     else if (a.H <= 8192) launch_int8<4, 4>(a, st);
