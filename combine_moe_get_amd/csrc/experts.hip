@@ -12,8 +12,8 @@
 //
 // A workgroup is persistent: it keeps a ring of stages in LDS filled by loads that go past the registers, and multiplies
 // one stage's operands while the next one's come from LDS, on to the next tile without a pause where the ring allows it.
-// Bounds: few rows an expert, the weights from memory (8 rows of 8 experts, 134 MB: 25 us, 5.4 TB/s; 16 of 32 in 4 bits,
-// 883 MB with their scales: 157 us, 5.6 TB/s).  Many rows: a stage of a 256 x 256 tile is 2048 cycles of matrix
+// Bounds: few rows an expert, the weights from memory (8 rows of 8 experts, 4096 -> 2 x 1024 bf16, 134 MB: 24.4 us, 5.5
+// TB/s; 128 rows over 64, 7168 -> 2 x 2048 in 4 bits, 883 MB with the scales: 157 us, 5.6 TB/s).  Many rows: a stage of a 256 x 256 tile is 2048 cycles of matrix
 // instructions on each SIMD and 2048 of LDS (64 KB in, 192 KB out, 128 bytes a cycle), which do not overlap wholly: 1.72
 // us, at the 1.95 GHz of such a load 3350.  16 x 2048 rows of 4096 -> 4096 870 us, 1.26 PFLOP/s (torch's plain product
 // of 8192: 1.37, of 16384: 1.61); int8 2.6 POP/s, 4 bits 4 PFLOP/s.
@@ -31,7 +31,6 @@ typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kKB = 128;                // bytes of k per stage of a row operand
 constexpr int kKR = 64;                 // rows of k per stage of a column operand
-constexpr int kGroup = 8;               // tiles along m that are walked together
 constexpr uint32_t kOut = 0x80000000u;  // a byte offset past every buffer resource here: reads zero
 
 // a raw buffer resource of `bytes` bytes (at most 2^31 - 1) at a wave-uniform address; the address has 48 bits
@@ -135,6 +134,9 @@ template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, 
 __global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 1 : 2) experts_kernel(ExpertsArgs a) {
   using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST, WIDE>;
   constexpr bool MX = C::MX;
+  // Tiles along m that are walked together, by an XCD's 32 workgroups: 8 with 4 along n; in wgrad, where an XCD has a
+  // piece of an expert's tiles, 4 with as many along n (64 x 1000 rows, 1024 -> 7168: 943 us, with 8 951).
+  constexpr int kGroup = OP == OP_WGRAD ? 4 : 8;
   extern __shared__ __align__(1024) char lds[];
   int *first = (int *)(lds + C::LDS);  // [E + 1] tiles along m before each expert
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
