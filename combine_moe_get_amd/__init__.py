@@ -1,8 +1,10 @@
 """MI355X-native MoE expert-parallel dispatch and combine.
 
 The routing layout, the optional int8 quantization, the scatter of routed
-token copies into expert-major receive rows and the weighted combine with
-zero / copy / constant experts run in hand-written HIP kernels for gfx950,
+token copies into expert-major receive rows, the experts' matrix products over
+those rows (bf16, int8, microscaled 4-bit; with their gradients) and the weighted
+combine with zero / copy / constant experts (with its gradient) run in
+hand-written HIP kernels for gfx950,
 behind the C ABI of include/moe_get.h (libmoe_get.so).  This package is the
 thin Python binding over that ABI plus seeded input generators.
 """

@@ -288,7 +288,7 @@ int moe_combine_capped(const moe_get_shape_t *shape, int32_t max_workgroups, con
  * nor written.  Offsets that do not ascend, or that pass `rows`, are cut to the buffers: nothing
  * outside them is touched, and what the rows then hold is unspecified. */
 typedef struct moe_experts_shape {
-  int64_t rows;          /* rows the row buffers hold: 0 <= rows < 2^31 */
+  int64_t rows;          /* rows the row buffers hold: 0 <= rows < 2^27 */
   int64_t rank_stride;   /* 0: compact rows; A > 0: windows of A rows, num_ranks * A <= rows */
   int32_t num_experts;   /* 1..2048, a multiple of num_ranks */
   int32_t num_ranks;     /* >= 1 */
@@ -323,7 +323,8 @@ int moe_experts_check_shape(const moe_experts_shape_t *shape, int32_t row_type);
  * BF16: products exact, summed in fp32.  INT8: summed exactly in int32, then scaled by the row's and
  * the output channel's scale in fp32.  MXFP4: blocks of 32 products scaled by both powers of two and
  * summed in fp32; a NaN scale makes every sum it enters NaN.  The activation works on the fp32 values;
- * one rounding to bf16 at the end.  x, w and out must be 16-byte aligned, float32 scales 4-byte.
+ * one rounding to bf16 at the end.  x, w and out must be 16-byte aligned, float32 scales 4-byte; MXFP4 scales
+ * may begin anywhere and are read in aligned words of four bytes (fastest: aligned, in_features % 128 == 0).
  * Results do not depend on the launch (no atomics; the order of each sum is fixed by the shape). */
 int moe_experts_matmul(const moe_experts_shape_t *shape, int32_t row_type, int32_t act, const void *x,
                        const void *row_scales, const void *w, const void *w_scales, const int32_t *expert_offsets,
