@@ -8,10 +8,12 @@
 //   zero, dropped or masked slot: nothing; w: 0
 // One workgroup a token: g is read once, every expert row once and every gradient row is written once, so memory
 // bounds it: 4096 tokens of 4096 with 8 of 64 experts (576 MB) 95 us, 6.1 TB/s; 128 tokens of 7168 (31 MB, mostly
-// from the caches) 11 us; with copy and constant experts see below.
-// The gradients of the constant experts' vectors are sums over tokens: a second kernel, one workgroup per
-// (expert, 64 columns), whose waves each take every sixteenth part of the slots in order and are added in
-// order, so that the result does not depend on the launch.
+// from the caches) 11 us.
+// The gradients of the constant experts' vectors are sums over tokens: the launch's first workgroups, one for each 64
+// columns of each of these experts, whose waves take equal parts of the tokens in order and are added in order, so
+// that the result depends on the shape alone.  They wait for one load after the other and not for the memory's rate,
+// and run beside the tokens': 4096 x 8 slots on 128 experts, 2 copy and 2 constant ones, rows of 4096 (570 MB): 104 us, 5.5
+// TB/s (in a kernel of their own, behind it: 22 us more; the next slots not under way meanwhile).
 #include "experts_internal.hpp"
 
 namespace moe {
@@ -32,6 +34,80 @@ __device__ __forceinline__ void unpack8g(const u32x4 &v, float *f) {
 
 enum : int { G_NONE = 0, G_ROUTED = 1, G_COPY = 2, G_CONST = 3 };
 
+// The constant experts' vectors: a workgroup 64 columns of one expert.  Wave v of the nw adds the slots of the v-th part
+// of the tokens, in order.  It looks at 512 slots at a time (the next 512 under way meanwhile), lists in LDS the ones
+// it is looking for and takes eight of them at a time.
+constexpr int kScan = 512, kTake = 8;
+__device__ __forceinline__ void const_grad(const CombineGradArgs &a, int b, char *lds) {
+  const CombineArgs &c = a.c;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  int *slot = (int *)lds + wave * kScan;  // the wave's own: its LDS accesses are in order
+  float *sg = (float *)((int *)lds + nw * kScan), *sq = sg + nw * 64;
+  const int ncol = (c.H + 63) / 64, k = b / ncol, h = (b - k * ncol) * 64 + lane;
+  const int id = c.E + c.Z + c.C + k;
+  const int per = (c.T + nw - 1) / nw, lo = wave * per < c.T ? wave * per : c.T, hi = lo + per < c.T ? lo + per : c.T;
+  const int s1 = hi * c.K;  // T K <= 2^24
+  float g = 0.0f, q = 0.0f;
+  int ids[kScan / 64], on[kScan / 64];
+  auto look = [&](int s0) {
+#pragma unroll
+    for (int i = 0; i < kScan / 64; ++i) {
+      const int s = s0 + i * 64 + lane;
+      ids[i] = s < s1 ? c.topk_idx[s] : -1;
+      on[i] = c.mask && s < s1 ? c.mask[s / c.K] : 1;
+    }
+  };
+  look(lo * c.K);
+  for (int s0 = lo * c.K; s0 < s1; s0 += kScan) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kScan / 64; ++i) {
+      const bool hit = ids[i] == id && on[i] != 0;
+      const uint64_t hits = ballot(hit);
+      if (hit) slot[n + popc_below(hits)] = s0 + i * 64 + lane;
+      n += __builtin_popcountll(hits);
+    }
+    look(s0 + kScan);
+    for (int i = 0; i < n; i += kTake) {
+      float w[kTake], gv[kTake], xv[kTake];
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        w[u] = gv[u] = xv[u] = 0.0f;
+        if (i + u < n) {
+          const int s = __builtin_amdgcn_readfirstlane(slot[i + u]);
+          w[u] = c.w[s];
+          if (h < c.H) {
+            const size_t at = (size_t)(s / c.K) * c.H + h;
+            gv[u] = __uint_as_float((uint32_t)a.go[at] << 16);
+            if (a.ga1) xv[u] = __uint_as_float((uint32_t)c.ori_x[at] << 16);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kTake; ++u) {
+        if (i + u < n) {
+          const float wg = w[u] * gv[u];
+          g += wg;
+          q = __builtin_fmaf(wg, xv[u], q);
+        }
+      }
+    }
+  }
+  sg[wave * 64 + lane] = g;
+  sq[wave * 64 + lane] = q;
+  __syncthreads();
+  if (wave == 0 && h < c.H) {
+    for (int v = 1; v < nw; ++v) {
+      g += sg[v * 64 + lane];
+      q += sq[v * 64 + lane];
+    }
+    const size_t at = (size_t)k * c.H + h;
+    if (a.ga1) a.ga1[at] = q;
+    if (a.ga2) a.ga2[at] = __uint_as_float((uint32_t)c.cv[at] << 16) * g;
+    if (a.gv) a.gv[at] = __uint_as_float((uint32_t)c.a2[at] << 16) * g;
+  }
+}
+
 // One workgroup a token, a thread one chunk of 8 elements (two a thread, in turn: 99 us for the 95 above, 8.4 for 6.7
 // on 16 tokens of 7168); threads past the row's end only take part in the sums.  The slots' kinds, rows and weights are
 // wave-uniform; every row is requested before the first is used.  KMAX: the least of 1, 2, 4, 8, 16 that holds the
@@ -40,8 +116,13 @@ enum : int { G_NONE = 0, G_ROUTED = 1, G_COPY = 2, G_CONST = 3 };
 template <int KMAX, bool SPECIAL>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;
+  extern __shared__ __align__(16) char lds[];
   __shared__ float part[16][KMAX];
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (SPECIAL && (int)blockIdx.x < a.vectors) {
+    const_grad(a, blockIdx.x, lds);
+    return;
+  }
+  const int t = blockIdx.x - (SPECIAL ? a.vectors : 0), tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int H = c.H, K = c.K, nch = H >> 3;
   const bool live = !c.mask || c.mask[t];
 
@@ -150,97 +231,26 @@ __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   }
 }
 
-// workgroup (64 columns, constant expert): 16 waves, wave v adds the slots of the v-th sixteenth of the tokens, in
-// order.  A wave looks at 512 slots at a time (eight loads under way), lists the ones it is looking for in LDS and
-// takes eight of them at a time.  4096 x 8 slots on 128 experts, 2 copy and 2 constant ones,
-// rows of 4096: 22 us, bound by the wait for each load in turn and not by memory; the other gradients of that call: 101 us
-// (570 MB, 5.6 TB/s).
-constexpr int kScan = 512, kTake = 8;
-__global__ void __launch_bounds__(1024) const_grad_kernel(CombineGradArgs a) {
-  const CombineArgs &c = a.c;
-  __shared__ int slot[16][kScan];
-  __shared__ float sg[16][64], sq[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int k = blockIdx.y, h = blockIdx.x * 64 + lane;
-  const int id = c.E + c.Z + c.C + k;
-  const int per = (c.T + 15) / 16, lo = wave * per < c.T ? wave * per : c.T, hi = lo + per < c.T ? lo + per : c.T;
-  const int s1 = hi * c.K;  // T K <= 2^24
-  float g = 0.0f, q = 0.0f;
-  for (int s0 = lo * c.K; s0 < s1; s0 += kScan) {
-    int ids[kScan / 64];
-#pragma unroll
-    for (int i = 0; i < kScan / 64; ++i) ids[i] = s0 + i * 64 + lane < s1 ? c.topk_idx[s0 + i * 64 + lane] : -1;
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kScan / 64; ++i) {
-      const int s = s0 + i * 64 + lane;
-      bool hit = ids[i] == id;
-      if (hit && c.mask) hit = c.mask[s / c.K] != 0;
-      const uint64_t hits = ballot(hit);
-      if (hit) slot[wave][n + popc_below(hits)] = s;
-      n += __builtin_popcountll(hits);
-    }
-    // the list is the wave's own: its LDS accesses are in order
-    for (int i = 0; i < n; i += kTake) {
-      float w[kTake], gv[kTake], xv[kTake];
-#pragma unroll
-      for (int u = 0; u < kTake; ++u) {
-        w[u] = gv[u] = xv[u] = 0.0f;
-        if (i + u < n) {
-          const int s = __builtin_amdgcn_readfirstlane(slot[wave][i + u]);
-          w[u] = c.w[s];
-          if (h < c.H) {
-            const size_t at = (size_t)(s / c.K) * c.H + h;
-            gv[u] = __uint_as_float((uint32_t)a.go[at] << 16);
-            if (a.ga1) xv[u] = __uint_as_float((uint32_t)c.ori_x[at] << 16);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kTake; ++u) {
-        if (i + u < n) {
-          const float wg = w[u] * gv[u];
-          g += wg;
-          q = __builtin_fmaf(wg, xv[u], q);
-        }
-      }
-    }
-  }
-  sg[wave][lane] = g;
-  sq[wave][lane] = q;
-  __syncthreads();
-  if (wave == 0 && h < c.H) {
-    for (int v = 1; v < 16; ++v) {
-      g += sg[v][lane];
-      q += sq[v][lane];
-    }
-    const size_t at = (size_t)k * c.H + h;
-    if (a.ga1) a.ga1[at] = q;
-    if (a.ga2) a.ga2[at] = __uint_as_float((uint32_t)c.cv[at] << 16) * g;
-    if (a.gv) a.gv[at] = __uint_as_float((uint32_t)c.a2[at] << 16) * g;
-  }
-}
-
 template <int KMAX>
 static void launch_k(const CombineGradArgs &a, hipStream_t st) {
-  const int nch = a.c.H >> 3;
-  const dim3 grid((unsigned)a.c.T), block((unsigned)((nch + 63) / 64 * 64));  // nch <= 1024
-  if (a.c.C + a.c.Kc > 0) hipLaunchKernelGGL((combine_grad_kernel<KMAX, true>), grid, block, 0, st, a);
+  const int nch = a.c.H >> 3;  // <= 1024
+  // at least 8 waves where they search the slots for constant experts
+  const unsigned threads = (unsigned)(a.vectors && nch < 512 ? 512 : (nch + 63) / 64 * 64);
+  const dim3 grid((unsigned)(a.vectors + (a.gy || a.gw || a.gx ? a.c.T : 0))), block(threads);
+  if (grid.x == 0) return;
+  const size_t lds = a.vectors ? threads / 64 * (kScan + 2 * 64) * 4 : 0;
+  if (a.c.C + a.c.Kc > 0) hipLaunchKernelGGL((combine_grad_kernel<KMAX, true>), grid, block, lds, st, a);
   else hipLaunchKernelGGL((combine_grad_kernel<KMAX, false>), grid, block, 0, st, a);
 }
 
-hipError_t launch_combine_grad(const CombineGradArgs &a, hipStream_t st) {
-  if (a.c.T > 0 && (a.gy || a.gw || a.gx)) {
-    if (a.c.K <= 1) launch_k<1>(a, st);
-    else if (a.c.K <= 2) launch_k<2>(a, st);
-    else if (a.c.K <= 4) launch_k<4>(a, st);
-    else if (a.c.K <= 8) launch_k<8>(a, st);
-    else launch_k<16>(a, st);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.c.Kc > 0 && (a.ga1 || a.ga2 || a.gv))  // T = 0: zeros
-    hipLaunchKernelGGL(const_grad_kernel, dim3((unsigned)((a.c.H + 63) / 64), (unsigned)a.c.Kc), dim3(1024), 0, st, a);
+hipError_t launch_combine_grad(const CombineGradArgs &a_, hipStream_t st) {
+  CombineGradArgs a = a_;
+  a.vectors = a.ga1 || a.ga2 || a.gv ? (a.c.H + 63) / 64 * a.c.Kc : 0;  // T = 0: they are zeros
+  if (a.c.K <= 1) launch_k<1>(a, st);
+  else if (a.c.K <= 2) launch_k<2>(a, st);
+  else if (a.c.K <= 4) launch_k<4>(a, st);
+  else if (a.c.K <= 8) launch_k<8>(a, st);
+  else launch_k<16>(a, st);
   return hipGetLastError();
 }
 

@@ -61,6 +61,7 @@ struct CombineGradArgs {
   float *gw;
   uint16_t *gx;
   float *ga1, *ga2, *gv;
+  int32_t vectors;       // workgroups for those three (set by the launcher)
 };
 hipError_t launch_combine_grad(const CombineGradArgs &a, hipStream_t stream);
 

@@ -162,6 +162,29 @@ def test_against_differences():
         assert abs(terms.sum() - (loss(*up) - loss(*down)) / 2) <= 2 * half * np.abs(terms).sum() + 1e-9
 
 
+@pytest.mark.parametrize("H", [72, 1032, 8192])
+def test_only_what_is_asked_for(H):
+    """Every subset of the six results is what the whole call gives; the others' buffers are not needed."""
+    T, K, E, C, Kc = 38, 4, 8, 2, 3
+    d = _world([6, H], T, H, K, E, 1, C, Kc, 0.8)
+    shape = mg.make_shape(T, H, K, E, 2, 1, C, Kc)
+    ids, m, w = G.dev(d["ids"]), G.dev(d["mask"]), G.dev(d["w"])
+    lay = mg.layout(shape, ids, m)
+    y = X.bf16(d["r"], T * K, H).to(X.DEV)
+    ins = [d[k].to(X.DEV) for k in ("go", "x", "a1", "a2", "v")]
+    call = mg.prepare_combine_grad(shape, ins[0], y, ids, w, lay.dst_row, m, *ins[1:], X.canary(T * K, H))
+    full = [t.clone() for t in call()]
+    at = range(11, 17)  # the results among the arguments
+    all_args = list(call._args)
+    for subset in range(1, 64):
+        for t in call.result:
+            t.fill_(-7)
+        for i, a in enumerate(at):
+            call._args[a] = all_args[a] if subset >> i & 1 else None
+        for i, (got, want) in enumerate(zip(call(), full)):
+            assert torch.equal(got, want if subset >> i & 1 else torch.full_like(got, -7)), (subset, i)
+
+
 def test_no_tokens():
     shape = mg.make_shape(0, 64, 2, 4, 2, 0, 0, 2)
     e = torch.empty(0, dtype=torch.bfloat16, device=X.DEV)
