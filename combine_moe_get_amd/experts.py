@@ -318,6 +318,7 @@ def combine_grad(shape, grad_out, expert_out, topk_idx, topk_weights, dst_row, x
     left as they were), grad_topk_weights (float32 [T, K]), grad_ori_x (bfloat16 [T, H]; None without
     copy and constant experts), grad_alpha1 / grad_alpha2 / grad_v (float32 [Kc, H]; None without
     constant experts).  `rows` as for combine().  The gradient of a bf16 dispatch is
-    combine(shape, grad_expand_x, topk_idx, ones, dst_row)."""
+    combine(shape, grad_expand_x, topk_idx, ones, dst_row), without special experts in the shape and
+    with -1 for their slots in topk_idx."""
     return prepare_combine_grad(shape, grad_out, expert_out, topk_idx, topk_weights, dst_row, x_active_mask, ori_x,
                                 const_alpha1, const_alpha2, const_v, grad_expert_out, rows)(stream)

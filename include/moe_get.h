@@ -368,7 +368,8 @@ int moe_quantize_rows(int32_t row_type, int64_t rows, int32_t features, const ui
  * for moe_combine.  Every output may be NULL and is then not computed (not all of them); expert_out is
  * needed only for grad_topk_weights.  Rows of grad_expert_out that dst_row does not name are left as
  * they were; all other outputs are written whole.  grad_out and the bf16 arrays 16-byte aligned.  The
- * gradient of bf16 moe_dispatch is moe_combine with unit weights.
+ * gradient of bf16 moe_dispatch is moe_combine of the rows' gradients with unit weights, on the shape
+ * without special experts and with -1 for their slots in topk_idx.
  *  out grad_expert_out [cap, H] bf16, grad_topk_weights [T, K] float32, grad_ori_x [T, H] bf16,
  *      grad_alpha1, grad_alpha2, grad_v [Kc, H] float32 */
 int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, const uint16_t *expert_out,

@@ -185,6 +185,21 @@ def test_only_what_is_asked_for(H):
             assert torch.equal(got, want if subset >> i & 1 else torch.full_like(got, -7)), (subset, i)
 
 
+def test_gradient_of_dispatch_beside_special_experts():
+    """The combine with unit weights and without the special experts: each token's rows added up."""
+    T, H, K, E, C, Kc = 48, 264, 4, 8, 2, 2
+    d = _world(7, T, H, K, E, 1, C, Kc, 0.8)
+    ids, m = G.dev(d["ids"]), G.dev(d["mask"])
+    lay = mg.layout(mg.make_shape(T, H, K, E, 2, 1, C, Kc), ids, m)
+    dst = lay.dst_row.cpu().numpy()
+    y = X.bf16(d["r"], T * K, H)
+    routed = torch.where(ids < E, ids, -1).contiguous()
+    got = mg.combine(mg.make_shape(T, H, K, E, 2), y.to(X.DEV), routed, torch.ones(T, K, device=X.DEV), lay.dst_row, m)
+    rows = np.where(dst[:, :, None] >= 0, X.f64(y)[np.maximum(dst, 0)], 0.0)
+    ref, err = rows.sum(1), K * X.STEP32 * np.abs(rows).sum(1)
+    _near(got, ref, err + X.BF16_HALF * (np.abs(ref) + err), "tokens")
+
+
 def test_no_tokens():
     shape = mg.make_shape(0, 64, 2, 4, 2, 0, 0, 2)
     e = torch.empty(0, dtype=torch.bfloat16, device=X.DEV)
