@@ -43,13 +43,16 @@ __device__ __forceinline__ i32x4 resource(const void *p, int64_t bytes) {
 
 // 64 lanes x 16 bytes from `off` + `soff` past the resource's base (behind its end: zeros) to LDS at `at` + `more` +
 // lane * 16; all but `off` wave-uniform.  Asm, because for its own loads into LDS the compiler waits before every
-// LDS read that it cannot prove disjoint, which here is each: stage_wait() waits instead.  No register is written.
+// LDS read that it cannot prove disjoint, which here is each: stage_wait() waits instead.  No vector register is written; M0 is,
+// which the unused result tells the compiler.
 // The wait states that a memory instruction needs are the statement's own, as the compiler does not see one in it: five
 // after a vector instruction's write of a scalar register that it reads (the readfirstlanes of resource(), or of an
 // operand here), the addition and four idle ones; M0 is good for it after one.
 __device__ __forceinline__ void load_to_lds(i32x4 d, uint32_t off, uint32_t soff, uint32_t at, uint32_t more) {
-  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off), "s"(d), "s"(soff),
-               "s"(at), "i"(more)
+  [[maybe_unused]] int m0;
+  asm volatile("s_add_u32 m0, %4, %5\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               : "={m0}"(m0)
+               : "v"(off), "s"(d), "s"(soff), "s"(at), "i"(more)
                : "memory", "scc");
 }
 

@@ -71,3 +71,15 @@ def test_loads_to_lds_keep_their_distance_from_the_descriptors_writes(kernels):
                     near.append(f"{name}: {distance(body, i)}")
     assert loads > 0
     assert not near, f"{len(near)} of {loads} loads, in {len({n.rsplit(':', 1)[0] for n in near})} kernels: {near[:4]}"
+
+
+def test_m0_is_the_loads_own(kernels):
+    """M0 holds the LDS address of the loads, written by each for itself: nothing else in such a kernel keeps a value
+    there or reads one."""
+    for name, body in kernels.items():
+        if not any(ins.startswith("buffer_load") and ins.endswith(" lds") for ins in body):
+            continue
+        uses = [i for i, ins in enumerate(body) if re.search(r"\bm0\b", ins)]
+        for i in uses:
+            assert body[i].startswith("s_add_u32 m0,") and "m0" not in body[i].split(",", 1)[1], (name, body[i])
+            assert any(ins.startswith("buffer_load") for ins in body[i + 1:i + 3]), (name, body[i:i + 3])
