@@ -16,8 +16,9 @@ from .binding import (  # noqa: F401
     prepare_layout_noalloc, rank_capacity, recv_capacity, status_string, workspace_size,
 )
 from .experts import (  # noqa: F401
-    ACT_NONE, ACT_SWIGLU, ROWS_BF16, ROWS_INT8, ROWS_MXFP4, CombineGrad, ExpertsCall, ExpertsShape,
-    check_experts_shape, combine_grad, experts_matmul, experts_matmul_dgrad, experts_matmul_wgrad,
-    make_experts_shape, prepare_combine_grad, prepare_experts_matmul, prepare_experts_matmul_dgrad,
-    prepare_experts_matmul_wgrad, prepare_quantize_rows, quantize_rows,
+    ACT_NONE, ACT_SWIGLU, EXPERTS_DGRAD, EXPERTS_FORWARD, EXPERTS_WGRAD, ROWS_BF16, ROWS_INT8, ROWS_MXFP4,
+    CombineGrad, ExpertsCall, ExpertsShape, check_experts_shape, combine_grad, experts_matmul,
+    experts_matmul_dgrad, experts_matmul_wgrad, experts_tile, make_experts_shape, prepare_combine_grad,
+    prepare_experts_matmul, prepare_experts_matmul_dgrad, prepare_experts_matmul_wgrad, prepare_quantize_rows,
+    quantize_rows,
 )

@@ -137,7 +137,7 @@ __device__ __forceinline__ int n_of(int p, int &half) {
 #define LAMBDA __attribute__((always_inline))
 
 template <int TY, int OP, bool GATED, bool F32, int BM, int BN, int WM, int WN, int NST, bool RING, bool WIDE>
-__global__ void __launch_bounds__(64 * WM *WN, WM *WN == 4 && BM *BN == 65536 ? 1 : 2) experts_kernel(ExpertsArgs a) {
+__global__ void __launch_bounds__(64 * WM *WN, 2) experts_kernel(ExpertsArgs a) {
   using C = Tile<TY, OP, GATED, F32, BM, BN, WM, WN, NST, WIDE>;
   constexpr bool MX = C::MX;
   // Tiles along m that are walked together, by an XCD's 32 workgroups: 8 with 4 along n; in wgrad, where an XCD has a
@@ -607,49 +607,60 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
 // The first, with scales at odd addresses (not WIDE), runs out of registers.  64 x 128 with two stages: 16 rows of 32
 // experts, 4096 -> 2 x 4096 in 98 us (four: 110); with four for at most 256 tiles: 8 of 8, 4096 -> 2 x 1024 in 11.8 us
 // (13.5).  Scales at odd addresses cost 106 us where these cost 98.
-template <int TY, int OP, bool GATED, bool F32, bool WIDE>
-static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
-  constexpr bool MX = TY == MOE_ROWS_MXFP4;
-  constexpr int E16 = TY == MOE_ROWS_BF16 ? 8 : TY == MOE_ROWS_INT8 ? 16 : 32;
-  const int64_t E = a.g.E, mean = (a.g.rows + E - 1) / E, m = OP == OP_WGRAD ? a.M : mean;
+ExpertsTile experts_tile(const ExpertsArgs &a, int op, int row_type, bool gated, bool wide) {
+  const bool mx = row_type == MOE_ROWS_MXFP4;
+  const int e16 = row_type == MOE_ROWS_BF16 ? 8 : row_type == MOE_ROWS_INT8 ? 16 : 32;
+  const int64_t E = a.g.E, mean = (a.g.rows + E - 1) / E, m = op == OP_WGRAD ? a.M : mean;
   auto tiles = [&](int bm, int bn) {
-    const int64_t co = GATED ? bn / 2 : bn;
+    const int64_t co = gated ? bn / 2 : bn;
     // ragged rows leave half a tile an expert empty
-    const int64_t mt = OP == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm;
+    const int64_t mt = op == OP_WGRAD ? E * ((m + bm - 1) / bm) : (a.g.rows + E * bm / 2) / bm;
     return mt * ((a.N + co - 1) / co);
   };
-  if constexpr (OP == OP_FORWARD && !MX) {
-    if (mean <= 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);
-  }
-  if (m <= 64) {
-    if (MX && tiles(64, 128) > 256) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 2, true, WIDE>(a, st);
-    return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 4, true, WIDE>(a, st);
-  }
-  const double stages = OP == OP_FORWARD ? (a.K / E16 + 7) / 8 : OP == OP_DGRAD ? (a.K + 63) / 64 : (mean + 63) / 64;
+  if (op == OP_FORWARD && !mx && mean <= 16) return {16, 64, 4};
+  if (m <= 64) return {64, 128, mx && tiles(64, 128) > 256 ? 2 : 4};
+  const double stages = op == OP_FORWARD ? (a.K / e16 + 7) / 8 : op == OP_DGRAD ? (a.K + 63) / 64 : (mean + 63) / 64;
   auto time = [&](int bm, int bn, int slots, double stage, double between) {
     const double rounds = (double)((tiles(bm, bn) + slots - 1) / slots), one = stages * stage + between;
-    const double largest = OP == OP_WGRAD ? (E < 3 ? E : 3) * stages * stage : 0.0;
+    const double largest = op == OP_WGRAD ? (E < 3 ? E : 3) * stages * stage : 0.0;
     return rounds * one > largest ? rounds * one : largest;
   };
   const double big = time(256, 256, 256, 1.72, 4.0), two = time(128, 128, 512, 1.15, 1.5);
-  if constexpr (MX) {
-    if constexpr (WIDE) {
-      if (big <= two) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
+  if (mx) return wide && big <= two ? ExpertsTile{256, 256, 2} : ExpertsTile{128, 128, 2};
+  const double flat = time(256, 128, 256, 0.93, 2.5), deep = time(128, 128, 256, 0.60, 2.0);
+  if (big <= two && big <= flat && big <= deep) return {256, 256, 2};
+  if (flat <= two && flat <= deep) return {256, 128, 3};
+  return {128, 128, deep <= two ? 4 : 2};
+}
+
+// the kernel of the tile; one is built only where experts_tile can name it
+template <int TY, int OP, bool GATED, bool F32, bool WIDE>
+static hipError_t launch_tile(const ExpertsArgs &a, hipStream_t st) {
+  constexpr bool MX = TY == MOE_ROWS_MXFP4;
+  const ExpertsTile t = experts_tile(a, OP, TY, GATED, WIDE);
+  if constexpr (OP == OP_FORWARD && !MX) {
+    if (t.rows == 16) return launch_cfg<TY, OP, GATED, F32, 16, 64, 1, 2, 4, true, true>(a, st);
+  }
+  if (t.rows == 64) {
+    if constexpr (MX) {
+      if (t.stages == 2) return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 2, true, WIDE>(a, st);
     }
-  } else {
-    const double wide = time(256, 128, 256, 0.93, 2.5), deep = time(128, 128, 256, 0.60, 2.0);
-    if (big <= two && big <= wide && big <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
-    if (wide <= two && wide <= deep) return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, WIDE>(a, st);
-    if (deep <= two) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, WIDE>(a, st);
+    return launch_cfg<TY, OP, GATED, F32, 64, 128, 2, 2, 4, true, WIDE>(a, st);
+  }
+  if constexpr (WIDE) {
+    if (t.columns == 256) return launch_cfg<TY, OP, GATED, F32, 256, 256, 2, 4, 2, false, WIDE>(a, st);
+  }
+  if constexpr (!MX) {
+    if (t.rows == 256) return launch_cfg<TY, OP, GATED, F32, 256, 128, 4, 2, 3, true, WIDE>(a, st);
+    if (t.stages == 4) return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 4, true, WIDE>(a, st);
   }
   return launch_cfg<TY, OP, GATED, F32, 128, 128, 2, 2, 2, true, WIDE>(a, st);
 }
 
-// MXFP4: whether every row of scales begins at a multiple of four bytes
 template <int TY, int OP, bool GATED, bool F32>
 static hipError_t launch_type(const ExpertsArgs &a, hipStream_t st) {
   if constexpr (TY == MOE_ROWS_MXFP4) {
-    if (a.K % 128 != 0 || (((uintptr_t)a.ms | (uintptr_t)a.ns) & 3) != 0) return launch_tile<TY, OP, GATED, F32, false>(a, st);
+    if (!mx_scales_wide(a.K, a.ms, a.ns)) return launch_tile<TY, OP, GATED, F32, false>(a, st);
   }
   return launch_tile<TY, OP, GATED, F32, true>(a, st);
 }

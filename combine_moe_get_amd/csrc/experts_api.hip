@@ -44,6 +44,17 @@ RowGroups groups(const moe_experts_shape_t *s, const int32_t *off) {
   return g;
 }
 
+// the sizes of a product's operands
+ExpertsArgs sizes(const moe_experts_shape_t *s, int op, const int32_t *off) {
+  ExpertsArgs a;
+  memset(&a, 0, sizeof a);
+  a.g = groups(s, off);
+  a.K = op == OP_FORWARD ? s->in_features : op == OP_DGRAD ? s->out_features : 0;
+  a.M = op == OP_WGRAD ? s->out_features : 0;
+  a.N = op == OP_FORWARD ? s->out_features : s->in_features;
+  return a;
+}
+
 int done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 }  // namespace
@@ -51,6 +62,20 @@ int done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 extern "C" {
 
 int moe_experts_check_shape(const moe_experts_shape_t *shape, int32_t row_type) { return check_shape(shape, row_type); }
+
+int moe_experts_tile(const moe_experts_shape_t *shape, int32_t op, int32_t row_type, int32_t act, int32_t tile[3]) {
+  const int st = check_shape(shape, row_type);
+  if (st != MOE_OK) return st;
+  if (!tile || op < MOE_EXPERTS_FORWARD || op > MOE_EXPERTS_WGRAD || (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU))
+    return MOE_ERR_ARG;
+  if (op != MOE_EXPERTS_FORWARD && (row_type != MOE_ROWS_BF16 || act != MOE_ACT_NONE)) return MOE_ERR_ARG;
+  const bool wide = row_type != MOE_ROWS_MXFP4 || mx_scales_wide(shape->in_features, nullptr, nullptr);
+  const ExpertsTile t = experts_tile(sizes(shape, op, nullptr), op, row_type, act == MOE_ACT_SWIGLU, wide);
+  tile[0] = t.rows;
+  tile[1] = t.columns;
+  tile[2] = t.stages;
+  return MOE_OK;
+}
 
 int moe_experts_matmul(const moe_experts_shape_t *shape, int32_t row_type, int32_t act, const void *x,
                        const void *row_scales, const void *w, const void *w_scales, const int32_t *expert_offsets,
@@ -65,16 +90,12 @@ int moe_experts_matmul(const moe_experts_shape_t *shape, int32_t row_type, int32
       !aligned(expert_offsets, 4))
     return MOE_ERR_ARG;
   if (row_type == MOE_ROWS_MXFP4 && (!row_scales || !w_scales)) return MOE_ERR_ARG;
-  ExpertsArgs a;
-  a.g = groups(shape, expert_offsets);
+  ExpertsArgs a = sizes(shape, OP_FORWARD, expert_offsets);
   a.m = x;
   a.n = w;
   a.ms = row_scales;
   a.ns = w_scales;
   a.out = out;
-  a.K = shape->in_features;
-  a.M = 0;
-  a.N = shape->out_features;
   return done(launch_experts(a, OP_FORWARD, row_type, act, false, (hipStream_t)stream));
 }
 
@@ -86,14 +107,10 @@ int moe_experts_matmul_dgrad(const moe_experts_shape_t *shape, const uint16_t *g
   if (!grad_out || !w || !expert_offsets || !grad_x || !aligned(grad_out, 16) || !aligned(w, 16) ||
       !aligned(grad_x, 16) || !aligned(expert_offsets, 4))
     return MOE_ERR_ARG;
-  ExpertsArgs a;
-  memset(&a, 0, sizeof a);
-  a.g = groups(shape, expert_offsets);
+  ExpertsArgs a = sizes(shape, OP_DGRAD, expert_offsets);
   a.m = grad_out;
   a.n = w;
   a.out = grad_x;
-  a.K = shape->out_features;
-  a.N = shape->in_features;
   return done(launch_experts(a, OP_DGRAD, MOE_ROWS_BF16, MOE_ACT_NONE, false, (hipStream_t)stream));
 }
 
@@ -104,14 +121,10 @@ int moe_experts_matmul_wgrad(const moe_experts_shape_t *shape, int32_t grad_w_fp
   if (grad_w_fp32 != 0 && grad_w_fp32 != 1) return MOE_ERR_ARG;
   if (!expert_offsets || !grad_w || !aligned(grad_w, 16) || !aligned(expert_offsets, 4)) return MOE_ERR_ARG;
   if (shape->rows > 0 && (!grad_out || !x || !aligned(grad_out, 16) || !aligned(x, 16))) return MOE_ERR_ARG;
-  ExpertsArgs a;
-  memset(&a, 0, sizeof a);
-  a.g = groups(shape, expert_offsets);
+  ExpertsArgs a = sizes(shape, OP_WGRAD, expert_offsets);
   a.m = grad_out;
   a.n = x;
   a.out = grad_w;
-  a.M = shape->out_features;
-  a.N = shape->in_features;
   return done(launch_experts(a, OP_WGRAD, MOE_ROWS_BF16, MOE_ACT_NONE, grad_w_fp32 != 0, (hipStream_t)stream));
 }
 

@@ -30,7 +30,11 @@ __device__ __forceinline__ void expert_rows(const RowGroups &g, int e, int64_t &
   n = (int)c;
 }
 
-enum ExpertsOp : int { OP_FORWARD = 0, OP_DGRAD = 1, OP_WGRAD = 2 };
+enum ExpertsOp : int {
+  OP_FORWARD = MOE_EXPERTS_FORWARD,
+  OP_DGRAD = MOE_EXPERTS_DGRAD,
+  OP_WGRAD = MOE_EXPERTS_WGRAD
+};
 
 struct ExpertsArgs {
   RowGroups g;
@@ -42,6 +46,17 @@ struct ExpertsArgs {
   int32_t M;             // wgrad: rows of a result (out_features)
   int32_t N;             // columns of the result
 };
+
+// The tile that a product runs on; wide: MXFP4 scales of a row begin at multiples of four bytes (else true).
+struct ExpertsTile {
+  int32_t rows, columns, stages;
+};
+ExpertsTile experts_tile(const ExpertsArgs &a, int op, int row_type, bool gated, bool wide);
+
+// MXFP4: whether every row of scales begins at a multiple of four bytes
+inline bool mx_scales_wide(int K, const void *ms, const void *ns) {
+  return K % 128 == 0 && (((uintptr_t)ms | (uintptr_t)ns) & 3) == 0;
+}
 
 hipError_t launch_experts(const ExpertsArgs &a, int op, int row_type, int act, bool out_fp32, hipStream_t stream);
 

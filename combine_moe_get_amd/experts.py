@@ -15,6 +15,7 @@ from . import binding as B
 
 ROWS_BF16, ROWS_INT8, ROWS_MXFP4 = 0, 1, 2
 ACT_NONE, ACT_SWIGLU = 0, 1
+EXPERTS_FORWARD, EXPERTS_DGRAD, EXPERTS_WGRAD = 0, 1, 2
 
 _TYPE_OF = {torch.bfloat16: ROWS_BF16, torch.int8: ROWS_INT8, torch.uint8: ROWS_MXFP4}
 U8 = (torch.uint8,)
@@ -52,6 +53,7 @@ def _lib():
         SP = ctypes.POINTER(ExpertsShape)
         for name, args in (
                 ("moe_experts_check_shape", [SP, I32]),
+                ("moe_experts_tile", [SP, I32, I32, I32, ctypes.POINTER(I32 * 3)]),
                 ("moe_experts_matmul", [SP, I32, I32] + [V] * 7),
                 ("moe_experts_matmul_dgrad", [SP] + [V] * 5),
                 ("moe_experts_matmul_wgrad", [SP, I32] + [V] * 5),
@@ -66,6 +68,15 @@ def _lib():
 def check_experts_shape(shape, row_type):
     """Status of moe_experts_check_shape: 0, or a negative MOE_ERR_*."""
     return _lib().moe_experts_check_shape(ctypes.byref(shape), int(row_type))
+
+
+def experts_tile(shape, op=EXPERTS_FORWARD, row_type=ROWS_BF16, act=ACT_NONE):
+    """(rows, columns, stages in LDS) of the tile that a product of this shape runs on (moe_experts_tile)."""
+    tile = (ctypes.c_int32 * 3)()
+    st = _lib().moe_experts_tile(ctypes.byref(shape), int(op), int(row_type), int(act), ctypes.byref(tile))
+    if st != B.MOE_OK:
+        raise B.MoeGetError("experts_tile", st)
+    return tuple(tile)
 
 
 class ExpertsCall(B.PreparedCall):

@@ -309,6 +309,16 @@ typedef struct moe_experts_shape {
 /* Validate an experts shape for rows of a type (MOE_ROWS_*). */
 int moe_experts_check_shape(const moe_experts_shape_t *shape, int32_t row_type);
 
+/* The three products of the stage. */
+#define MOE_EXPERTS_FORWARD 0  /* moe_experts_matmul */
+#define MOE_EXPERTS_DGRAD 1    /* moe_experts_matmul_dgrad (bf16 rows, MOE_ACT_NONE) */
+#define MOE_EXPERTS_WGRAD 2    /* moe_experts_matmul_wgrad (likewise) */
+
+/* The tile of the result that a workgroup of that product computes at a time: its rows, its columns (with
+ * MOE_ACT_SWIGLU of both halves together) and the stages of the contraction kept in LDS.  It follows from the shape,
+ * the type and the activation alone (for MXFP4 with scales at multiples of four bytes).  For profiling and tests. */
+int moe_experts_tile(const moe_experts_shape_t *shape, int32_t op, int32_t row_type, int32_t act, int32_t tile[3]);
+
 /* out[r, n] = act( sum_k x[r, k] w[e][n, k] ), e the expert of row r.
  *  row_type           MOE_ROWS_*: the type of x and of w
  *  act                MOE_ACT_*
