@@ -5,7 +5,7 @@ import re
 import pytest
 
 import combine_moe_get_amd as mg
-from tests import _isa
+from tests import _isa, _tiles
 
 PRODUCTS = [(mg.EXPERTS_FORWARD, t, a) for t in (mg.ROWS_BF16, mg.ROWS_INT8, mg.ROWS_MXFP4)
             for a in (mg.ACT_NONE, mg.ACT_SWIGLU)]
@@ -48,3 +48,14 @@ def test_tile_refuses():
             mg.experts_tile(s, *bad)
     with pytest.raises(mg.MoeGetError):
         mg.experts_tile(mg.make_experts_shape(64, 8, 72, 24), 0, mg.ROWS_INT8)
+
+
+@pytest.mark.parametrize("case", _tiles.CASES, ids=_tiles.name)
+def test_sizes_that_are_run_for_a_tile_select_it(case):
+    op, ty, act, tile, E, mean, k, n = case
+    assert mg.experts_tile(_tiles.rows_of(E, mean).shape(k, n), op, ty, act) == tile
+
+
+def test_every_tile_has_sizes_that_are_run():
+    run = {(ty, op, act, tile, ty != mg.ROWS_MXFP4 or k % 128 == 0) for op, ty, act, tile, _, _, k, _ in _tiles.CASES}
+    assert run == _selected()
