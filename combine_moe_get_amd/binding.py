@@ -72,6 +72,36 @@ class PreparedCall:
         return self.result
 
 
+def _tensors(of):
+    """The tensors of a call's result or arguments: a tensor, or tuples of them among other things."""
+    if isinstance(of, torch.Tensor):
+        return [of]
+    return [t for o in of for t in _tensors(o)] if isinstance(of, tuple) else []
+
+
+def call_on(stream, prepare, *args):
+    """prepare(*args) and issue the call on `stream` (None: the current one); returns its result.
+
+    On another stream than the current one, what the call allocates comes from that stream's memory, and the
+    allocator is told that the arguments are used there and the results on the current stream: the caller may drop
+    any of them at once.  Ordering stays the caller's: `stream` has to wait for what the arguments' values wait
+    for, and readers of the results have to wait for `stream`."""
+    if stream is None:
+        return prepare(*args)()
+    current = torch.cuda.current_stream(stream.device)
+    if stream == current:
+        return prepare(*args)(stream)
+    with torch.cuda.stream(stream):
+        call = prepare(*args)
+        out = call(stream)
+    for t in _tensors(call._keep):
+        t.record_stream(stream)
+    for t in _tensors(out):  # one that the caller gave is used on both
+        t.record_stream(stream)
+        t.record_stream(current)
+    return out
+
+
 _lib = None
 
 

@@ -4,7 +4,9 @@ expert, their gradients, row quantization and the combine's gradient.
 As in binding.py: argument checks and marshalling only, outputs allocated with PyTorch unless
 given, every step in the HIP kernels, no CPU fallback.  All tensors of a call must be on one
 device; the call runs on that device's current stream (or the given one of that device),
-whichever device is current.
+whichever device is current.  With `stream=` arguments and results may be dropped at once (binding.call_on);
+a prepare_* call makes its results in the memory of the stream that is current then, keeps its tensors
+alive itself, and is to be kept until what it issued on other streams is done.
 """
 import ctypes
 from collections import namedtuple
@@ -174,7 +176,7 @@ def experts_matmul(shape, x, w, expert_offsets, row_scales=None, w_scales=None, 
       w_scales   int8: float32 [E, Nw] (None: ones); MXFP4: uint8 [E, Nw, in / 32]
       expert_offsets  int32 [E + 1] of the layout
     Returns out [rows, out_features] bfloat16; rows of no expert are left as they were."""
-    return prepare_experts_matmul(shape, x, w, expert_offsets, row_scales, w_scales, act, out)(stream)
+    return B.call_on(stream, prepare_experts_matmul, shape, x, w, expert_offsets, row_scales, w_scales, act, out)
 
 
 def prepare_experts_matmul_dgrad(shape, grad_out, w, expert_offsets, out=None):
@@ -199,7 +201,7 @@ def prepare_experts_matmul_dgrad(shape, grad_out, w, expert_offsets, out=None):
 def experts_matmul_dgrad(shape, grad_out, w, expert_offsets, out=None, stream=None):
     """moe_experts_matmul_dgrad: the gradient grad_out[r] w[e] [rows, in_features] of the bf16
     product's rows (shape as given to experts_matmul).  Rows of no expert are left as they were."""
-    return prepare_experts_matmul_dgrad(shape, grad_out, w, expert_offsets, out)(stream)
+    return B.call_on(stream, prepare_experts_matmul_dgrad, shape, grad_out, w, expert_offsets, out)
 
 
 def prepare_experts_matmul_wgrad(shape, grad_out, x, expert_offsets, dtype=torch.bfloat16, out=None):
@@ -229,7 +231,7 @@ def experts_matmul_wgrad(shape, grad_out, x, expert_offsets, dtype=torch.bfloat1
     """moe_experts_matmul_wgrad: the gradient grad_out^T x over each expert's rows
     [E, out_features, in_features] of the bf16 product's weights, in dtype (bfloat16 or float32;
     that of out if given).  Zeros for experts without rows."""
-    return prepare_experts_matmul_wgrad(shape, grad_out, x, expert_offsets, dtype, out)(stream)
+    return B.call_on(stream, prepare_experts_matmul_wgrad, shape, grad_out, x, expert_offsets, dtype, out)
 
 
 def prepare_quantize_rows(x, row_type, codes=None, scales=None, shape=None, expert_offsets=None):
@@ -273,7 +275,7 @@ def quantize_rows(x, row_type, codes=None, scales=None, shape=None, expert_offse
     [...]) or ROWS_MXFP4 (uint8 codes [..., features / 2], uint8 scales [..., features / 32]).  With
     shape and expert_offsets only rows that belong to an expert are touched; without, all (weights).
     Returns (codes, scales)."""
-    return prepare_quantize_rows(x, row_type, codes, scales, shape, expert_offsets)(stream)
+    return B.call_on(stream, prepare_quantize_rows, x, row_type, codes, scales, shape, expert_offsets)
 
 
 CombineGrad = namedtuple("CombineGrad", ["grad_expert_out", "grad_topk_weights", "grad_ori_x", "grad_alpha1",
@@ -331,5 +333,5 @@ def combine_grad(shape, grad_out, expert_out, topk_idx, topk_weights, dst_row, x
     constant experts).  `rows` as for combine().  The gradient of a bf16 dispatch is
     combine(shape, grad_expand_x, topk_idx, ones, dst_row), without special experts in the shape and
     with -1 for their slots in topk_idx."""
-    return prepare_combine_grad(shape, grad_out, expert_out, topk_idx, topk_weights, dst_row, x_active_mask, ori_x,
-                                const_alpha1, const_alpha2, const_v, grad_expert_out, rows)(stream)
+    return B.call_on(stream, prepare_combine_grad, shape, grad_out, expert_out, topk_idx, topk_weights, dst_row,
+                     x_active_mask, ori_x, const_alpha1, const_alpha2, const_v, grad_expert_out, rows)

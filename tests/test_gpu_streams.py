@@ -1,0 +1,70 @@
+"""Calls on a stream that is not the current one, whose arguments and results the caller drops at once while the
+stream is still busy with something else."""
+import numpy as np
+import pytest
+import torch
+
+import combine_moe_get_amd as mg
+from tests import _experts as X
+from tests import _gpu as G
+
+pytestmark = pytest.mark.gpu
+
+T, H, I, K, E = 64, 256, 128, 4, 8
+
+
+def _world():
+    r = np.random.default_rng(21)
+    b = lambda *s: X.bf16(r, *s).to(X.DEV)  # noqa: E731
+    shape = mg.make_shape(T, H, K, E, 2, 0, 1, 1)
+    ids = G.dev(np.argsort(r.random((T, E + 2)), axis=1)[:, :K].astype(np.int32))
+    lay = mg.layout(shape, ids)
+    s = mg.make_experts_shape(T * K, E, H, I)
+    return dict(shape=shape, s=s, ids=ids, dst=lay.dst_row, off=lay.expert_offsets, w=G.dev(r.random((T, K)).astype(np.float32)),
+                x=b(T, H), y=b(T * K, H), rows=b(T * K, H), wt=b(E, I, H), dy=b(T * K, I), a=[b(1, H) for _ in range(3)])
+
+
+# the arguments that a call reads, and the call
+CALLS = {
+    "experts_matmul": (("rows", "wt", "off"),
+                       lambda d, t, s: mg.experts_matmul(d["s"], t["rows"], t["wt"], t["off"], stream=s)),
+    "experts_matmul_dgrad": (("dy", "wt", "off"),
+                             lambda d, t, s: mg.experts_matmul_dgrad(d["s"], t["dy"], t["wt"], t["off"], stream=s)),
+    "experts_matmul_wgrad": (("dy", "rows", "off"),
+                             lambda d, t, s: mg.experts_matmul_wgrad(d["s"], t["dy"], t["rows"], t["off"], stream=s)),
+    "quantize_rows": (("rows",), lambda d, t, s: mg.quantize_rows(t["rows"], mg.ROWS_INT8, stream=s)),
+    "combine_grad": (("x", "y", "ids", "w", "dst"),
+                     lambda d, t, s: mg.combine_grad(d["shape"], t["x"], t["y"], t["ids"], t["w"], t["dst"], None, t["x"],
+                                                     *d["a"], stream=s)[1:]),
+}
+
+
+def _tensors(out):
+    return [out] if isinstance(out, torch.Tensor) else [t for o in out for t in _tensors(o)] if isinstance(out, tuple) else []
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_arguments_and_results_dropped_at_once(name):
+    d = _world()
+    keys, call = CALLS[name]
+    used = int(d["off"][-1])
+    cut = lambda t: t[:used] if t.shape[0] == T * K else t  # noqa: E731  rows of no expert: not written
+    want = [cut(t).clone() for t in _tensors(call(d, d, None))]
+    side, spin = torch.cuda.Stream(), 20_000_000  # some 10 ms
+    for _ in range(3):
+        t = {k: d[k].clone() for k in keys}
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(spin)
+        out = _tensors(call(d, t, side))
+        spare = _tensors(call(d, t, side))
+        taken = {o.data_ptr() for o in spare} | {v.data_ptr() for v in t.values()}
+        sizes = [(o.shape, o.dtype) for o in spare] + [(v.shape, v.dtype) for v in t.values()]
+        del spare, t
+        fresh = [torch.ones(s, dtype=dt, device=X.DEV) for s, dt in sizes for _ in range(2)]
+        if not side.query():  # still under way: its memory must not be handed out
+            assert not taken & {f.data_ptr() for f in fresh}
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(cut(o), w) for o, w in zip(out, want))
+        assert all(bool((f == 1).all()) for f in fresh)
