@@ -325,14 +325,14 @@ def layout_noalloc(shape, topk_idx, x_active_mask=None, out=None, stream=None, r
     """moe_get_layout_noalloc: the layout of layout(), its workspace in the library's static
     device scratch (no allocation in the library; raises MoeGetError with status -6 when the
     shape needs more than noalloc_scratch_bytes())."""
-    return prepare_layout_noalloc(shape, topk_idx, x_active_mask, out, rank_stride)(stream)
+    return call_on(stream, prepare_layout_noalloc, shape, topk_idx, x_active_mask, out, rank_stride)
 
 
 def layout(shape, topk_idx, x_active_mask=None, out=None, workspace=None, stream=None, rank_stride=0):
     """moe_get_layout (rank_stride 0) or moe_get_layout_ex.  Returns a Layout of device
     tensors; `status` is a sticky int32 word (bit 1: an out-of-range expert id was dropped;
     bit 2: a copy did not fit its rank window)."""
-    return prepare_layout(shape, topk_idx, x_active_mask, out, workspace, rank_stride)(stream)
+    return call_on(stream, prepare_layout, shape, topk_idx, x_active_mask, out, workspace, rank_stride)
 
 
 def prepare_dispatch(shape, quant_mode, x, dst_row, x_smooth_scale=None, topk_weights=None, topk_idx=None,
@@ -380,8 +380,8 @@ def dispatch(shape, quant_mode, x, dst_row, x_smooth_scale=None, topk_weights=No
     expand_weights [rows] or None); rows not named by dst_row are left as they were.
     `rows` (default T * K) sizes the outputs allocated here; a fixed-capacity layout
     needs P * rank_stride.  max_workgroups > 0 caps the grid (moe_dispatch_capped)."""
-    return prepare_dispatch(shape, quant_mode, x, dst_row, x_smooth_scale, topk_weights, topk_idx,
-                            expand_x, dynamic_scales, expand_weights, rows, max_workgroups)(stream)
+    return call_on(stream, prepare_dispatch, shape, quant_mode, x, dst_row, x_smooth_scale, topk_weights, topk_idx,
+                   expand_x, dynamic_scales, expand_weights, rows, max_workgroups)
 
 
 def prepare_combine(shape, expert_out, topk_idx, topk_weights, dst_row, x_active_mask=None, ori_x=None,
@@ -423,8 +423,8 @@ def combine(shape, expert_out, topk_idx, topk_weights, dst_row, x_active_mask=No
     must hold (default T * K, which covers every compact layout; a fixed-capacity layout needs
     P * rank_stride; a caller that knows N may pass rows=N).  max_workgroups > 0 caps the grid
     (moe_combine_capped)."""
-    return prepare_combine(shape, expert_out, topk_idx, topk_weights, dst_row, x_active_mask, ori_x,
-                           const_alpha1, const_alpha2, const_v, out, rows, max_workgroups)(stream)
+    return call_on(stream, prepare_combine, shape, expert_out, topk_idx, topk_weights, dst_row, x_active_mask, ori_x,
+                   const_alpha1, const_alpha2, const_v, out, rows, max_workgroups)
 
 
 def _smooth_rows(shape, x_smooth_scale):
@@ -491,5 +491,5 @@ def layout_dispatch(shape, quant_mode, x, topk_idx, x_active_mask=None, x_smooth
     slots; above that the layout kernels, which also read x ahead into the GPU's caches, then
     the dispatch kernel).  Returns (Layout, expand_x, dynamic_scales or None, expand_weights or
     None), identical to layout() followed by dispatch()."""
-    return prepare_layout_dispatch(shape, quant_mode, x, topk_idx, x_active_mask, x_smooth_scale, topk_weights,
-                                   out, expand_x, dynamic_scales, expand_weights, workspace, rank_stride)(stream)
+    return call_on(stream, prepare_layout_dispatch, shape, quant_mode, x, topk_idx, x_active_mask, x_smooth_scale,
+                   topk_weights, out, expand_x, dynamic_scales, expand_weights, workspace, rank_stride)

@@ -77,3 +77,12 @@ def test_the_functions_go_this_way(name, monkeypatch):
     f = getattr(experts, name)
     f(*[None] * (2 if name == "quantize_rows" else 6 if name == "combine_grad" else 4), stream="s")
     assert seen == [("s", getattr(experts, "prepare_" + name))]
+
+
+@pytest.mark.parametrize("name,required", [("layout", 2), ("layout_noalloc", 2), ("dispatch", 4), ("combine", 5),
+                                           ("layout_dispatch", 4)])
+def test_the_layers_functions_go_this_way(name, required, monkeypatch):
+    seen = []
+    monkeypatch.setattr(B, "call_on", lambda stream, prepare, *args: seen.append((stream, prepare)))
+    getattr(B, name)(*[None] * required, stream="s")
+    assert seen == [("s", getattr(B, "prepare_" + name))]

@@ -68,3 +68,35 @@ def test_arguments_and_results_dropped_at_once(name):
         torch.cuda.synchronize()
         assert all(torch.equal(cut(o), w) for o, w in zip(out, want))
         assert all(bool((f == 1).all()) for f in fresh)
+
+
+def test_a_layer_on_a_side_stream():
+    """Layout (whose status word is cleared by the call), dispatch and combine on a stream that is busy, with the workspace
+    and the arguments gone."""
+    d = _world()
+    shape = mg.make_shape(T, H, K, E, 2)
+    ids, x, w = (d[k].clone() for k in ("ids", "x", "w"))
+    ids[ids >= E] = -1
+
+    def layer(ids, x, w, s):
+        lay, ex, _, _ = mg.layout_dispatch(shape, mg.QUANT_NONE, x, ids, stream=s)
+        again = mg.layout(shape, ids, stream=s)
+        ex2 = mg.dispatch(shape, mg.QUANT_NONE, x, again.dst_row, stream=s)[0]
+        noalloc = mg.layout_noalloc(shape, ids, stream=s)
+        out = mg.combine(shape, ex2, ids, w, noalloc.dst_row, stream=s)
+        n = int((ids >= 0).sum())
+        return [lay.dst_row, lay.status, again.dst_row, again.status, noalloc.status, ex[:n], ex2[:n], out]
+
+    want = [t.clone() for t in layer(ids, x, w, None)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        args = [t.clone() for t in (ids, x, w)]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        got = layer(*args, side)
+        del args
+        fresh = [torch.full((n,), 3, dtype=torch.int32, device=X.DEV) for n in (1, 1, 1, T * K, T * K, T * H // 2, 1 << 16)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(bool((f == 3).all()) for f in fresh)
