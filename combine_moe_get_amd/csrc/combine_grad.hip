@@ -13,7 +13,9 @@
 // columns of each of these experts, whose waves take equal parts of the tokens in order and are added in order, so
 // that the result depends on the shape alone.  They wait for one load after the other and not for the memory's rate,
 // and run beside the tokens': 4096 x 8 slots on 128 experts, 2 copy and 2 constant ones, rows of 4096 (570 MB): 104 us, 5.5
-// TB/s (in a kernel of their own, behind it: 22 us more; the next slots not under way meanwhile).
+// TB/s (in a kernel of their own, behind it: 22 us more; the next slots not under way meanwhile).  Each of them looks at
+// all ids, so the work grows with the number of these experts: made for few (4096 tokens of 8192, top 8 of 128 and 2, 16
+// or 64 constant ones: 233, 320, 555 us).
 #include "experts_internal.hpp"
 
 namespace moe {
@@ -112,7 +114,8 @@ __device__ __forceinline__ void const_grad(const CombineGradArgs &a, int b, char
 // on 16 tokens of 7168); threads past the row's end only take part in the sums.  The slots' kinds, rows and weights are
 // wave-uniform; every row is requested before the first is used.  KMAX: the least of 1, 2, 4, 8, 16 that holds the
 // slots (K = 8 with 16: 12.5 us for 128 tokens of 7168, 10.7 with 8).  SPECIAL: copy and constant experts can occur;
-// without them there is no x to read.
+// without them there is no x to read; with them every token reads its x, also one that has no such slot (two of 132
+// experts each, top 8: four of five; some 5% of the bytes).
 template <int KMAX, bool SPECIAL>
 __global__ void __launch_bounds__(1024) combine_grad_kernel(CombineGradArgs a) {
   const CombineArgs &c = a.c;

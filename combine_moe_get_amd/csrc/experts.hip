@@ -12,11 +12,12 @@
 //
 // A workgroup is persistent: it keeps a ring of stages in LDS filled by loads that go past the registers, and multiplies
 // one stage's operands while the next one's come from LDS, on to the next tile without a pause where the ring allows it.
-// Bounds: few rows an expert, the weights from memory (8 rows of 8 experts, 4096 -> 2 x 1024 bf16, 134 MB: 24.4 us, 5.5
-// TB/s; 128 rows over 64, 7168 -> 2 x 2048 in 4 bits, 883 MB with the scales: 157 us, 5.6 TB/s).  Many rows: a stage of a 256 x 256 tile is 2048 cycles of matrix
-// instructions on each SIMD and 2048 of LDS (64 KB in, 192 KB out, 128 bytes a cycle), which do not overlap wholly: 1.72
-// us, at the 1.95 GHz of such a load 3350.  16 x 2048 rows of 4096 -> 4096 870 us, 1.26 PFLOP/s (torch's plain product
-// of 8192: 1.37, of 16384: 1.61); int8 2.6 POP/s, 4 bits 4 PFLOP/s.
+// Bounds: few rows an expert, the weights from memory (8 rows of 8 of 64 experts, 4096 -> 2 x 1024 bf16, 134 MB: 24.9 us,
+// 5.4 TB/s; 128 rows over 64, 7168 -> 2 x 2048 in 4 bits, 883 MB with the scales: 156 us, 5.7 TB/s).  Many rows: a stage
+// of a 256 x 256 tile is 2048 cycles of matrix instructions on each SIMD and 2048 of LDS (64 KB in, 192 KB out, 128 bytes
+// a cycle), which do not overlap wholly: 1.72 us, at the 1.95 GHz of such a load 3350.  16 x 2048 rows of 4096 -> 4096
+// 840 to 870 us, 1.26 to 1.31 PFLOP/s (torch's plain product of 8192: 1.37, of 16384: 1.61); int8 465 us, 2.4 POP/s,
+// 4 bits 307 us, 3.6 PFLOP/s; the gradients 830 and 901.
 #include "experts_internal.hpp"
 
 namespace moe {
@@ -595,19 +596,20 @@ static hipError_t launch_cfg(const ExpertsArgs &a, hipStream_t st) {
   hipLaunchKernelGGL(k, dim3(grid), dim3(C::T), lds, st, a);
   return hipGetLastError();
 }
-// The tile: 16 x 64 for forward with at most 16 rows an expert (weights streamed once, three workgroups a CU: 8 rows of
-// 8 experts, 4096 -> 2 x 1024 bf16 in 22 us; 64 x 128: 23, 128 x 128: 28), 64 x 128 for at most 64; else what comes
+// The tile, for `rows` rows spread evenly over the experts (the counts are on the device): 16 x 64 for forward with at most
+// 16 an expert (weights streamed once, three workgroups a CU: 8 rows of 8 of 64 experts, 4096 -> 2 x 1024 bf16 in 24.9
+// us; 64 x 128: 28.9, 128 x 128: 32.9), 64 x 128 for at most 64; else what comes
 // out fastest by rounds of tiles over the CUs x (stages x time of a stage + time between tiles), measured in us
 // on one MI355X where the tiles fill the chip:
 //                                               stage  between   16 x 2048 rows, 4096 -> 4096 bf16
-//   256 x 256, 8 waves, two stages, one a CU     1.72     4      870 us
-//   256 x 128, 8 waves, three stages, one a CU   0.93     2.5    957   (an expert's few rows in one tile, its waves
+//   256 x 256, 8 waves, two stages, one a CU     1.72     4      870 us (the four in turn, as below)
+//   256 x 128, 8 waves, three stages, one a CU   0.93     2.5    976   (an expert's few rows in one tile, its waves
 //                                                                      without rows idle)
-//   128 x 128, 4 waves, two stages, two a CU     1.15     1.5    1175
-//   128 x 128, 4 waves, four stages, one a CU    0.60     2      1173  (deep: for hardly more tiles than CUs)
+//   128 x 128, 4 waves, two stages, two a CU     1.15     1.5    1091
+//   128 x 128, 4 waves, four stages, one a CU    0.60     2      1199  (deep: for hardly more tiles than CUs)
 // The order that it gives is that of the measured times within 15 % on 1024 to 32768 rows of 4 to 64 experts (128 rows
-// of each of 4, 4096 -> 2 x 2048 bf16, in the table's order: 79, 45, 57, 41 us; 200 of 32, 2048 -> 1024: 62, 46, 50,
-// 49).  In wgrad a tile costs what its expert has rows: the largest is taken to have three times the mean.
+// of each of 4, 4096 -> 2 x 2048 bf16, in the table's order: 84, 52, 63, 48 us; 200 of 32, 2048 -> 1024: 57, 41, 46,
+// 46).  In wgrad a tile costs what its expert has rows: the largest is taken to have three times the mean.
 //   MXFP4 has the first and the third.  A stage's scales are a load more where they are read stage by stage, which three
 // and four stages would need: the fourth took 36 us against 32 for the third on 128 rows of 4 experts, 4128 -> 2 x 2048.
 // The first, with scales at odd addresses (not WIDE), runs out of registers.  64 x 128 with two stages: 16 rows of 32

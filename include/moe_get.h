@@ -286,9 +286,17 @@ int moe_combine_capped(const moe_get_shape_t *shape, int32_t max_workgroups, con
  * cut at the end of the window.  How many rows each expert has is read on the device: any number,
  * none included.  Rows of no expert (behind the last, or behind a window's last) are neither read
  * nor written.  Offsets that do not ascend, or that pass `rows`, are cut to the buffers: nothing
- * outside them is touched, and what the rows then hold is unspecified. */
+ * outside them is touched, and what the rows then hold is unspecified.
+ *
+ * Outputs may not overlap inputs or one another.
+ *
+ * Speed: the host does not see the counts, so the products choose their tiles (moe_experts_tile) as if all `rows`
+ * were in use, rows / num_experts an expert.  Windows of the full capacity hold few: 256 experts on 32 ranks,
+ * 7168 -> 2 x 2048 bf16 with the gate, compact rows against windows of moe_get_rank_capacity, us: 128 tokens
+ * 2398 / 2361, 1024 tokens 2433 / 2851, 4096 tokens 3912 / 3202.  moe_quantize_rows visits every row that
+ * there is room for: 7 / 28, 34 / 189, 138 / 806 to MXFP4.  Where that matters, give tight windows or compact rows. */
 typedef struct moe_experts_shape {
-  int64_t rows;          /* rows the row buffers hold: 0 <= rows < 2^27 */
+  int64_t rows;          /* rows the row buffers hold: 0 <= rows < 2^27 (also steers the speed, see above) */
   int64_t rank_stride;   /* 0: compact rows; A > 0: windows of A rows, num_ranks * A <= rows */
   int32_t num_experts;   /* 1..2048, a multiple of num_ranks */
   int32_t num_ranks;     /* >= 1 */
@@ -379,7 +387,9 @@ int moe_quantize_rows(int32_t row_type, int64_t rows, int32_t features, const ui
  * needed only for grad_topk_weights.  Rows of grad_expert_out that dst_row does not name are left as
  * they were; all other outputs are written whole.  grad_out and the bf16 arrays 16-byte aligned.  The
  * gradient of bf16 moe_dispatch is moe_combine of the rows' gradients with unit weights, on the shape
- * without special experts and with -1 for their slots in topk_idx.
+ * without special experts and with -1 for their slots in topk_idx.  The constant experts' sums look at all T K ids
+ * once for every 64 columns of each of them: made for few (4096 tokens of 8192, top 8 of 128 and Kc, all results:
+ * 217 us without, 233 with 2, 320 with 16, 555 with 64).
  *  out grad_expert_out [cap, H] bf16, grad_topk_weights [T, K] float32, grad_ori_x [T, H] bf16,
  *      grad_alpha1, grad_alpha2, grad_v [Kc, H] float32 */
 int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, const uint16_t *expert_out,
