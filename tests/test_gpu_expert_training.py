@@ -1,5 +1,5 @@
-"""A training step of a gated layer as the README writes it: the first product without the gate, the activation and its
-gradient in torch, everything else in the library; against autograd in 64 bits."""
+"""A training step of a gated layer: the first product without the gate, the activation and its gradient in torch,
+everything else in the library; against autograd in 64 bits."""
 import numpy as np
 import pytest
 import torch

@@ -100,3 +100,32 @@ def test_a_layer_on_a_side_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(bool((f == 3).all()) for f in fresh)
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_captured_on_a_stream_that_joins_the_capture(name):
+    """Two calls on a side stream inside a capture, the first one's results dropped there; replayed with eager work and
+    synchronizations between the replays."""
+    d = _world()
+    keys, call = CALLS[name]
+    used = int(d["off"][-1])
+    cut = lambda t: t[:used] if t.shape[0] == T * K else t  # noqa: E731  rows of no expert: not written
+    call(d, d, None)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    t = {k: d[k].clone() for k in keys}
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(d, t, side)
+        got = _tensors(call(d, t, side))
+        torch.cuda.current_stream().wait_stream(side)
+    for k in range(3):
+        for key, v in t.items():
+            if v.dtype == torch.bfloat16:
+                v.copy_(d[key] * (k + 1))
+        want = [cut(w).clone() for w in _tensors(call(d, t, None))]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(cut(g), w) for g, w in zip(got, want)), k
+        torch.ones(1 << 20, device=X.DEV).sum()
