@@ -55,6 +55,26 @@ ExpertsArgs sizes(const moe_experts_shape_t *s, int op, const int32_t *off) {
   return a;
 }
 
+// the sizes, rows and weights that the gate and its gradient have in common
+int swiglu_args(int64_t rows, int32_t features, const float *row_weights, const moe_experts_shape_t *shape,
+                const int32_t *expert_offsets, SwigluArgs &a) {
+  if (rows < 0 || features <= 0) return MOE_ERR_SHAPE;
+  if (features > 65536 || features % 8 != 0 || rows >= ((int64_t)1 << 42) / features) return MOE_ERR_UNSUPPORTED;
+  memset(&a, 0, sizeof a);
+  if (shape || expert_offsets) {
+    const int st = check_groups(shape);
+    if (st != MOE_OK) return st;
+    if (shape->rows != rows || shape->in_features != features) return MOE_ERR_SHAPE;
+    if (!expert_offsets || !aligned(expert_offsets, 4)) return MOE_ERR_ARG;
+    a.g = groups(shape, expert_offsets);
+  }
+  if (!aligned(row_weights, 4)) return MOE_ERR_ARG;
+  a.w = row_weights;
+  a.rows = rows;
+  a.I = features;
+  return MOE_OK;
+}
+
 int done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 }  // namespace
@@ -152,6 +172,46 @@ int moe_quantize_rows(int32_t row_type, int64_t rows, int32_t features, const ui
   a.rows = rows;
   a.H = features;
   return done(launch_rows_quant(a, row_type, (hipStream_t)stream));
+}
+
+int moe_swiglu(int64_t rows, int32_t features, const uint16_t *h0, const float *row_weights,
+               const moe_experts_shape_t *shape, const int32_t *expert_offsets, uint16_t *out, int8_t *codes,
+               float *scales, void *stream) {
+  SwigluArgs a;
+  const int st = swiglu_args(rows, features, row_weights, shape, expert_offsets, a);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!h0 || !out || !aligned(h0, 16) || !aligned(out, 16) || !codes != !scales || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return MOE_ERR_ARG;
+  a.h0 = h0;
+  a.out = out;
+  a.codes = codes;
+  a.scales = scales;
+  return done(launch_swiglu(a, (hipStream_t)stream));
+}
+
+int moe_swiglu_grad(int64_t rows, int32_t features, const uint16_t *grad_out, const uint16_t *h0, const int8_t *codes,
+                    const float *scales, const float *row_weights, const moe_experts_shape_t *shape,
+                    const int32_t *expert_offsets, uint16_t *grad_h0, uint16_t *out, float *grad_row_weights,
+                    void *stream) {
+  SwigluArgs a;
+  const int st = swiglu_args(rows, features, row_weights, shape, expert_offsets, a);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!grad_out || !aligned(grad_out, 16) || !codes != !scales || !h0 == !codes || !aligned(h0, 16) ||
+      !aligned(codes, 16) || !aligned(scales, 4))
+    return MOE_ERR_ARG;
+  if ((!grad_h0 && !out && !grad_row_weights) || !aligned(grad_h0, 16) || !aligned(out, 16) || !aligned(grad_row_weights, 4))
+    return MOE_ERR_ARG;
+  a.go = grad_out;
+  a.h0 = h0;
+  a.codes = const_cast<int8_t *>(codes);
+  a.scales = const_cast<float *>(scales);
+  a.gh0 = grad_h0;
+  a.out = out;
+  a.gw = grad_row_weights;
+  return done(launch_swiglu_grad(a, (hipStream_t)stream));
 }
 
 int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, const uint16_t *expert_out,

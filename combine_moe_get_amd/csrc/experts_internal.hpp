@@ -1,5 +1,5 @@
 // experts_internal.hpp -- argument blocks and launchers of the expert stage (experts.hip,
-// rows_quant.hip, combine_grad.hip) shared with its entry points (experts_api.hip).
+// rows_quant.hip, swiglu.hip, combine_grad.hip) shared with its entry points (experts_api.hip).
 #pragma once
 
 #include "moe_internal.hpp"
@@ -28,6 +28,15 @@ __device__ __forceinline__ void expert_rows(const RowGroups &g, int e, int64_t &
   c = c < 0 ? 0 : c > end - at ? end - at : c;
   lo = at;
   n = (int)c;
+}
+
+// whether row r (of all rows the buffers hold) belongs to an expert
+__device__ __forceinline__ bool row_used(const RowGroups &g, int64_t r) {
+  if (!g.off) return true;
+  if (g.stride <= 0) return r >= g.off[0] && r < g.off[g.E];
+  const uint32_t w = (uint32_t)r / (uint32_t)g.stride;  // fewer than 2^27 rows where there are groups
+  if ((int64_t)w * g.L >= g.E) return false;  // behind the last window
+  return r - (int64_t)w * g.stride < (int64_t)g.off[(w + 1) * g.L] - g.off[w * g.L];
 }
 
 enum ExpertsOp : int {
@@ -68,6 +77,20 @@ struct RowsQuantArgs {
   int32_t H;
 };
 hipError_t launch_rows_quant(const RowsQuantArgs &a, int row_type, hipStream_t stream);
+
+struct SwigluArgs {
+  RowGroups g;           // off null: every row
+  const uint16_t *h0, *go;
+  const float *w;
+  int8_t *codes;         // forward: written or null; gradient: read or null (then h0 is)
+  float *scales;
+  uint16_t *out, *gh0;
+  float *gw;
+  int64_t rows;
+  int32_t I;
+};
+hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t stream);
+hipError_t launch_swiglu_grad(const SwigluArgs &a, hipStream_t stream);
 
 struct CombineGradArgs {
   CombineArgs c;         // the combine's inputs (out unused)

@@ -12,15 +12,6 @@
 
 namespace moe {
 
-// whether row r (of all rows the buffers hold) belongs to an expert
-__device__ __forceinline__ bool row_used(const RowGroups &g, int64_t r) {
-  if (!g.off) return true;
-  if (g.stride <= 0) return r >= g.off[0] && r < g.off[g.E];
-  const int64_t w = r / g.stride;
-  if (w * g.L >= g.E) return false;  // behind the last window
-  return r - w * g.stride < (int64_t)g.off[(w + 1) * g.L] - g.off[w * g.L];
-}
-
 // the e2m1 code of v (|v| finite)
 __device__ __forceinline__ uint32_t e2m1(float v) {
   const float a = fabsf(v);

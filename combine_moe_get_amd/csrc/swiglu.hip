@@ -1,0 +1,198 @@
+// swiglu.hip -- the gate between the two products of a layer that trains, silu(g) u with routing weights, and its
+// gradient; between the two the gate's input may be kept in 8 bits.
+#include "dispatch_dev.hpp"
+#include "experts_internal.hpp"
+
+namespace moe {
+
+// The logistic function of g as a product s1 s2, and 1 - it: with t = exp(-|g| / 2), R = 1 / (1 + t t): R 1 for g >= 0, t R t
+// below, where what is multiplied between the two factors keeps its digits although exp(g) alone may be too small for fp32
+// (t is the square of exp(-|g| / 4), which is good down to |g| = 349).  1 - s is never taken as a difference.
+struct Logistic {
+  float s1, s2, rest;
+};
+__device__ __forceinline__ Logistic logistic(float g) {
+  const float q = __builtin_amdgcn_exp2f(fabsf(g) * (-0.25f * 1.44269504088896341f)), t = q * q, n = t * t;
+  const float R = __builtin_amdgcn_rcpf(1.0f + n);
+  return g >= 0.0f ? Logistic{R, 1.0f, n * R} : Logistic{t * R, t, R};
+}
+
+__device__ __forceinline__ uint32_t pack2s(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)a, (__bf16)b};  // round to nearest even, NaN stays NaN
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ u32x4 pack8(const float *f) {
+  return u32x4{pack2s(f[0], f[1]), pack2s(f[2], f[3]), pack2s(f[4], f[5]), pack2s(f[6], f[7])};
+}
+
+// the largest over a row of 16 lanes, to each of them
+__device__ __forceinline__ float max16(float v) {
+  auto fold = [&](auto ctrl) {
+    const int b = __float_as_int(v);
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(b, b, decltype(ctrl)::value, 0xf, 0xf, false)));
+  };
+  fold(std::integral_constant<int, 0xb1>{});   // quad_perm 1 0 3 2
+  fold(std::integral_constant<int, 0x4e>{});   // quad_perm 2 3 0 1
+  fold(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  fold(std::integral_constant<int, 0x140>{});  // row_mirror
+  return v;
+}
+
+constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is left
+
+// ---- forward: 16 lanes a block of 128 columns of a row, 8 of each half a lane -----------------------
+constexpr int kFwdBlocks = 2;  // blocks of 128 columns that a thread has under way
+template <bool KEEP>
+__global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
+  const int sub = threadIdx.x & 15, I = a.I;
+  const uint32_t nb = (uint32_t)(I + 127) / 128;
+  for (uint64_t first = (uint64_t)blockIdx.x * (16 * kFwdBlocks); first < (uint64_t)a.rows * nb;
+       first += (uint64_t)gridDim.x * (16 * kFwdBlocks)) {
+    const uint64_t row0 = first / nb;
+    const uint32_t rem = (uint32_t)(first - row0 * nb);
+    int64_t r[kFwdBlocks];
+    uint32_t b[kFwdBlocks];
+    bool in[kFwdBlocks];
+    u32x4 gv[kFwdBlocks], uv[kFwdBlocks];
+    float w[kFwdBlocks];
+#pragma unroll
+    for (int k = 0; k < kFwdBlocks; ++k) {
+      const uint32_t i = rem + k * 16 + (threadIdx.x >> 4), q = i / nb;
+      r[k] = (int64_t)row0 + q;
+      b[k] = i - q * nb;
+      const int col = (int)b[k] * 128 + sub * 8;
+      in[k] = r[k] < a.rows && row_used(a.g, r[k]) && col < I;
+      gv[k] = uv[k] = u32x4{0u, 0u, 0u, 0u};
+      w[k] = 1.0f;
+      if (in[k]) {
+        const uint16_t *p = a.h0 + r[k] * 2 * I + col;
+        gv[k] = *(const u32x4 *)p;
+        uv[k] = *(const u32x4 *)(p + I);
+        if (a.w) w[k] = a.w[r[k]];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFwdBlocks; ++k) {
+      const int col = (int)b[k] * 128 + sub * 8;
+      float g[8], u[8], h[8];
+      unpack8(gv[k], g);
+      unpack8(uv[k], u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const Logistic s = logistic(g[e]);
+        h[e] = s.s1 * g[e] * u[e] * s.s2 * w[k];
+      }
+      if (in[k]) *(u32x4 *)(a.out + r[k] * I + col) = pack8(h);
+      if constexpr (KEEP) {
+        auto keep = [&](const float *x, int half) {
+          float m = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+          m = max16(m);
+          const float dyn = m > 0.0f ? 127.0f * (1.0f / m) : 0.0f;
+          if (!in[k]) return;
+          int c[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) c[e] = sat_code(x[e] * dyn);
+          *(u32x2 *)(a.codes + r[k] * 2 * I + half * I + col) =
+              u32x2{pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7])};
+          if (sub == 0) a.scales[(r[k] * 2 + half) * nb + b[k]] = m > 0.0f ? 1.0f / dyn : 0.0f;
+        };
+        keep(g, 0);
+        keep(u, 1);
+      }
+    }
+  }
+}
+
+// ---- backward: L threads a row ------------------------------------------------------------------------
+__device__ __forceinline__ void unpack_codes(u32x2 v, float scale, float *f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = (float)((int)(v[e >> 2] << (24 - 8 * (e & 3))) >> 24) * scale;
+}
+
+template <int L, bool KEPT>
+__global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
+  __shared__ float red[2][4];
+  int par = 0;
+  const int lane = threadIdx.x % L, I = a.I, nch = I >> 3;
+  const uint32_t nb = (uint32_t)(I + 127) / 128;
+  constexpr int R = 256 / L;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R) {
+    const int64_t r = r0 + threadIdx.x / L;
+    const bool used = r < a.rows && row_used(a.g, r);
+    float dot = 0.0f;
+    if (used) {
+      const float w = a.w ? a.w[r] : 1.0f;
+      for (int c = lane; c < nch; c += L) {
+        float g[8], u[8], d[8], dg[8], du[8], h[8];
+        unpack8(((const u32x4 *)(a.go + r * I))[c], d);
+        if constexpr (KEPT) {
+          const int8_t *p = a.codes + r * 2 * I + c * 8;
+          const float *s = a.scales + r * 2 * nb + (c >> 4);
+          unpack_codes(*(const u32x2 *)p, s[0], g);
+          unpack_codes(*(const u32x2 *)(p + I), s[nb], u);
+        } else {
+          const uint16_t *p = a.h0 + r * 2 * I + c * 8;
+          unpack8(*(const u32x4 *)p, g);
+          unpack8(*(const u32x4 *)(p + I), u);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const Logistic s = logistic(g[e]);
+          const float wd = w * d[e], act = s.s1 * g[e];
+          du[e] = act * wd * s.s2;
+          dg[e] = s.s1 * u[e] * wd * s.s2 * __builtin_fmaf(g[e], s.rest, 1.0f);
+          const float hu = act * u[e] * s.s2;
+          h[e] = hu * w;
+          dot = __builtin_fmaf(d[e], hu, dot);
+        }
+        if (a.gh0) {
+          *(u32x4 *)(a.gh0 + r * 2 * I + c * 8) = pack8(dg);
+          *(u32x4 *)(a.gh0 + r * 2 * I + I + c * 8) = pack8(du);
+        }
+        if (a.out) *(u32x4 *)(a.out + r * I + c * 8) = pack8(h);
+      }
+    }
+    if (a.gw) {
+#pragma unroll
+      for (int s = (L < 64 ? L : 64) / 2; s > 0; s >>= 1) dot += __shfl_xor(dot, s);
+      if constexpr (L > 64) {
+        if ((threadIdx.x & 63) == 0) red[par][threadIdx.x >> 6] = dot;
+        __syncthreads();
+        dot = (red[par][0] + red[par][1]) + (red[par][2] + red[par][3]);
+        par ^= 1;
+      }
+      if (used && lane == 0) a.gw[r] = dot;
+    }
+  }
+}
+
+hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  const uint64_t blocks = (uint64_t)a.rows * ((a.I + 127) / 128);
+  const uint64_t wg = (blocks + 16 * kFwdBlocks - 1) / (16 * kFwdBlocks);
+  const dim3 grid((unsigned)(wg < kMostGroups ? wg : kMostGroups)), block(256);
+  if (a.codes) hipLaunchKernelGGL((swiglu_kernel<true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((swiglu_kernel<false>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int L>
+static void launch_grad(const SwigluArgs &a, hipStream_t st) {
+  const uint64_t wg = ((uint64_t)a.rows + 256 / L - 1) / (256 / L);
+  const dim3 grid((unsigned)(wg < kMostGroups ? wg : kMostGroups)), block(256);
+  if (a.codes) hipLaunchKernelGGL((swiglu_grad_kernel<L, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((swiglu_grad_kernel<L, false>), grid, block, 0, st, a);
+}
+
+hipError_t launch_swiglu_grad(const SwigluArgs &a, hipStream_t st) {
+  if (a.rows == 0) return hipSuccess;
+  if (a.I <= 128) launch_grad<16>(a, st);
+  else if (a.I <= 1024) launch_grad<64>(a, st);
+  else launch_grad<256>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe

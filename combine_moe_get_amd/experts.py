@@ -60,6 +60,8 @@ def _lib():
                 ("moe_experts_matmul_dgrad", [SP] + [V] * 5),
                 ("moe_experts_matmul_wgrad", [SP, I32] + [V] * 5),
                 ("moe_quantize_rows", [I32, I64, I32, V, V, V, SP, V, V]),
+                ("moe_swiglu", [I64, I32, V, V, SP, V, V, V, V, V]),
+                ("moe_swiglu_grad", [I64, I32, V, V, V, V, V, SP, V, V, V, V, V]),
                 ("moe_combine_grad", [ctypes.POINTER(B.Shape)] + [V] * 17)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, ctypes.c_int
@@ -276,6 +278,115 @@ def quantize_rows(x, row_type, codes=None, scales=None, shape=None, expert_offse
     shape and expert_offsets only rows that belong to an expert are touched; without, all (weights).
     Returns (codes, scales)."""
     return B.call_on(stream, prepare_quantize_rows, x, row_type, codes, scales, shape, expert_offsets)
+
+
+Swiglu = namedtuple("Swiglu", ["out", "codes", "scales"])
+SwigluGrad = namedtuple("SwigluGrad", ["grad_h0", "out", "grad_row_weights"])
+I8 = (torch.int8,)
+
+
+def _gate_rows(t, name, halves):
+    """(rows, features) of a tensor of rows that hold `halves` times the features."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, {'2 * ' if halves == 2 else ''}features]")
+    rows, n = t.shape
+    if n == 0 or n % (8 * halves):
+        raise ValueError(f"the rows of {name} hold {n} elements: a multiple of {8 * halves} is needed")
+    return rows, n // halves
+
+
+def prepare_swiglu(h0, row_weights=None, checkpoint=False, shape=None, expert_offsets=None, out=None, codes=None,
+                   scales=None):
+    """Checked, marshalled moe_swiglu call; see swiglu()."""
+    dev = _device_of(h0, "h0")
+    rows, n = _gate_rows(h0, "h0", 2)
+    if (shape is None) != (expert_offsets is None):
+        raise ValueError("shape and expert_offsets go together")
+    if (codes is not None or scales is not None) and not checkpoint:
+        raise ValueError("codes and scales are results of a checkpoint")
+    nb = (n + 127) // 128
+    if out is None:
+        out = torch.empty((rows, n), dtype=torch.bfloat16, device=dev)
+    if checkpoint:
+        if codes is None:
+            codes = torch.empty((rows, 2 * n), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty((rows, 2, nb), dtype=torch.float32, device=dev)
+    args = [
+        rows, n,
+        _ptr(h0, "h0", B.BF16, None, dev),
+        _ptr(row_weights, "row_weights", B.F32, rows, dev, required=False),
+        ctypes.byref(shape) if shape is not None else None,
+        _ptr(expert_offsets, "expert_offsets", B.I32, shape.num_experts + 1 if shape is not None else None, dev,
+             required=False),
+        _ptr(out, "out", B.BF16, rows * n, dev),
+        _ptr(codes, "codes", I8, rows * 2 * n, dev, required=False),
+        _ptr(scales, "scales", B.F32, rows * 2 * nb, dev, required=False),
+        None,
+    ]
+    return ExpertsCall(_lib().moe_swiglu, args, "swiglu", (h0, row_weights, shape, expert_offsets),
+                       Swiglu(out, codes, scales), dev)
+
+
+def swiglu(h0, row_weights=None, checkpoint=False, shape=None, expert_offsets=None, out=None, codes=None, scales=None,
+           stream=None):
+    """moe_swiglu: out[r] = row_weights[r] silu(g) u of the rows h0[r] = [g | u], bfloat16 [rows, 2 * features].
+      row_weights  float32 [rows] (dispatch's expand_weights; None: ones)
+      checkpoint   also keep h0 in 8 bits for swiglu_grad: codes int8 [rows, 2 * features] and scales float32
+                   [rows, 2, ceil(features / 128)]
+      shape, expert_offsets  of the second product (in_features = features): only rows of experts are touched;
+                   both None: all rows
+    Returns a Swiglu(out [rows, features] bfloat16, codes, scales); the last two None without a checkpoint."""
+    return B.call_on(stream, prepare_swiglu, h0, row_weights, checkpoint, shape, expert_offsets, out, codes, scales)
+
+
+def prepare_swiglu_grad(grad_out, h0=None, codes=None, scales=None, row_weights=None, shape=None, expert_offsets=None,
+                        grad_h0=None, out=None, grad_row_weights=None, need_out=True):
+    """Checked, marshalled moe_swiglu_grad call; see swiglu_grad()."""
+    dev = _device_of(grad_out, "grad_out")
+    rows, n = _gate_rows(grad_out, "grad_out", 1)
+    if (shape is None) != (expert_offsets is None):
+        raise ValueError("shape and expert_offsets go together")
+    if (codes is None) != (scales is None) or (h0 is None) == (codes is None):
+        raise ValueError("either h0 or codes and scales are needed")
+    if out is not None and not need_out:
+        raise ValueError("out is given but need_out is not set")
+    nb = (n + 127) // 128
+    if grad_h0 is None:
+        grad_h0 = torch.empty((rows, 2 * n), dtype=torch.bfloat16, device=dev)
+    if out is None and need_out:
+        out = torch.empty((rows, n), dtype=torch.bfloat16, device=dev)
+    if grad_row_weights is None and row_weights is not None:
+        grad_row_weights = torch.empty(rows, dtype=torch.float32, device=dev)
+    args = [
+        rows, n,
+        _ptr(grad_out, "grad_out", B.BF16, None, dev),
+        _ptr(h0, "h0", B.BF16, rows * 2 * n, dev, required=False),
+        _ptr(codes, "codes", I8, rows * 2 * n, dev, required=False),
+        _ptr(scales, "scales", B.F32, rows * 2 * nb, dev, required=False),
+        _ptr(row_weights, "row_weights", B.F32, rows, dev, required=False),
+        ctypes.byref(shape) if shape is not None else None,
+        _ptr(expert_offsets, "expert_offsets", B.I32, shape.num_experts + 1 if shape is not None else None, dev,
+             required=False),
+        _ptr(grad_h0, "grad_h0", B.BF16, rows * 2 * n, dev),
+        _ptr(out, "out", B.BF16, rows * n, dev, required=False),
+        _ptr(grad_row_weights, "grad_row_weights", B.F32, rows, dev, required=False),
+        None,
+    ]
+    return ExpertsCall(_lib().moe_swiglu_grad, args, "swiglu_grad",
+                       (grad_out, h0, codes, scales, row_weights, shape, expert_offsets),
+                       SwigluGrad(grad_h0, out, grad_row_weights), dev)
+
+
+def swiglu_grad(grad_out, h0=None, codes=None, scales=None, row_weights=None, shape=None, expert_offsets=None,
+                grad_h0=None, out=None, grad_row_weights=None, need_out=True, stream=None):
+    """moe_swiglu_grad: the gradients of swiglu() for the gradient grad_out [rows, features] of its result, from h0 or
+    from its checkpoint (codes and scales).
+    Returns a SwigluGrad: grad_h0 (bfloat16 [rows, 2 * features]), out (the forward's result again, for the second
+    product's weight gradient; None with need_out=False), grad_row_weights (float32 [rows]; None without row_weights).
+    Rows of no expert are left as they were."""
+    return B.call_on(stream, prepare_swiglu_grad, grad_out, h0, codes, scales, row_weights, shape, expert_offsets,
+                     grad_h0, out, grad_row_weights, need_out)
 
 
 CombineGrad = namedtuple("CombineGrad", ["grad_expert_out", "grad_topk_weights", "grad_ori_x", "grad_alpha1",

@@ -399,6 +399,121 @@ int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, con
                      float *grad_topk_weights, uint16_t *grad_ori_x, float *grad_alpha1, float *grad_alpha2,
                      float *grad_v, void *stream);
 
+/* The gate between the two products of a layer that trains: row r of h0 holds [g | u], 2 * features elements, and
+ *   out[r, i] = row_weights[r] silu(g_i) u_i        (row_weights NULL: ones), in fp32, rounded once to bf16.
+ * With the routing weights here (moe_dispatch's expand_weights) the combine takes ones, and its backward pass does
+ * not need the experts' results: moe_swiglu_grad gives the weights' gradient.
+ * For the backward pass h0 may be kept in 8 bits (a checkpoint): codes and scales, both NULL or both given.  Each half
+ * of a row is cut into blocks of 128 elements (the last may be shorter).  Per block dyn = 127 (1 / amax), scale = 1 / dyn,
+ * code = round-half-even(x dyn) in [-127, 127], each operation rounded once to binary32 (amax 0: codes 0, scale 0; NaN
+ * counts nowhere and gets code 0; beside an infinity every code is 0 and the scale infinite); a code stands for code scale.
+ *  rows, features          0 <= rows, features a multiple of 8, at most 65536, rows * features < 2^42
+ *  shape, expert_offsets   both NULL: every row; else only the rows that belong to an expert of the layout
+ *                          (shape->rows = rows, shape->in_features = features: the second product's; out_features is
+ *                          not looked at); the others are neither read nor written
+ *  in  h0 [rows, 2 * features] bf16, row_weights [rows] float32 or NULL
+ *  out out [rows, features] bf16
+ *  out codes [rows, 2 * features] int8, scales [rows, 2, ceil(features / 128)] float32, or NULL
+ * h0, out and codes 16-byte aligned. */
+int moe_swiglu(int64_t rows, int32_t features, const uint16_t *h0, const float *row_weights,
+               const moe_experts_shape_t *shape, const int32_t *expert_offsets, uint16_t *out, int8_t *codes,
+               float *scales, void *stream);
+
+/* Gradient of moe_swiglu, from h0 or from its checkpoint (one of the two, the other NULL).  With d = grad_out[r],
+ * w = row_weights[r] and s = 1 / (1 + exp(-g)):
+ *   grad_h0[r] = [ w d u s (1 + g (1 - s)) | w d g s ], grad_row_weights[r] = sum_i d_i g_i s_i u_i,
+ *   out[r] = w g s u: the forward's result again, for the second product's weight gradient (from a checkpoint: of the
+ *   values that it holds).
+ * fp32 throughout, bf16 results rounded once.  Every output may be NULL and is then not computed (not all of them).
+ *  in  grad_out [rows, features] bf16
+ *  out grad_h0 [rows, 2 * features] bf16, out [rows, features] bf16, grad_row_weights [rows] float32 */
+int moe_swiglu_grad(int64_t rows, int32_t features, const uint16_t *grad_out, const uint16_t *h0, const int8_t *codes,
+                    const float *scales, const float *row_weights, const moe_experts_shape_t *shape,
+                    const int32_t *expert_offsets, uint16_t *grad_h0, uint16_t *out, float *grad_row_weights,
+                    void *stream);
+
+/* ---- the router: which experts a token goes to, the balance loss, their gradients ---------------------------
+ *
+ * What makes topk_idx and topk_weights out of the logits of a router.  An id is a column of the logits: with special
+ * experts num_ids = Etot.  An id is available to a token if its logit, and its bias if there is one, is neither NaN
+ * nor -inf; a logit of +inf counts as the largest finite one.  A token is live if x_active_mask (NULL: ones) has it and
+ * one of its logits is neither NaN nor -inf; the logits of masked tokens are not looked at. */
+typedef struct moe_route_shape {
+  int32_t num_tokens;   /* T: 0 <= T < 2^24 */
+  int32_t num_ids;      /* E: 1..2048 */
+  int32_t topk;         /* K: 1..16, at most topk_groups * num_ids / num_groups */
+  int32_t num_groups;   /* 1..64, divides num_ids */
+  int32_t topk_groups;  /* 1..num_groups: groups that a token's ids may come from */
+  int32_t group_score;  /* MOE_GROUP_* */
+  int32_t score;        /* MOE_SCORE_* */
+  int32_t renormalize;  /* 0, or 1: the weights of a token's slots are divided by their sum */
+  float scale;          /* what the weights are then multiplied by (finite) */
+} moe_route_shape_t;
+
+#define MOE_SCORE_SOFTMAX 0 /* s[t, e] = exp(l[t, e]) / sum over the ids with a logit */
+#define MOE_SCORE_SIGMOID 1 /* s[t, e] = 1 / (1 + exp(-l[t, e])) */
+#define MOE_GROUP_MAX 0     /* a group's score is its best key */
+#define MOE_GROUP_TOP2 1    /* the sum of its two best keys (of one, if only one is available) */
+
+int moe_route_check_shape(const moe_route_shape_t *shape);
+
+/* The router's choice.  Keys: with a bias or MOE_GROUP_TOP2 s[t, e] + bias[e], computed and compared in 64 bits (scores of
+ * 32 would let their rounding choose; keys within some 1e-15 of one another may come in either order); otherwise the
+ * logits, which have the same order.  The topk_groups best groups; of their ids the K best, in descending order.  Ties go
+ * to the lowest group or id.  The bias chooses only:
+ *   topk_weights[t, j] = scale * s[t, e_j]          (renormalize: s[t, e_j] / sum_i s[t, e_i], exact where both underflow)
+ * Slots for which no id is left hold -1 (which the layout drops) and weight 0; so do all slots of tokens that are not live.
+ *  logits_fp32        1: logits are float32, 0: bf16
+ *  in  logits [T, E], 16-byte aligned
+ *  in  bias [E] float32 or NULL, x_active_mask [T] uint8 or NULL
+ *  out topk_idx [T, K] int32, topk_weights [T, K] float32 */
+int moe_route(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const float *bias,
+              const uint8_t *x_active_mask, int32_t *topk_idx, float *topk_weights, void *stream);
+
+/* The losses that keep a router balanced.  The tokens are cut into `segments` equal runs (the batch, ranks, sequences) that
+ * are balanced each for itself.  With p[t, e] = s[t, e] / sum_e s[t, e] and, over the live tokens t of segment g,
+ *   T_g their number, c[g, e] the slots of topk_idx that hold e, P[g, e] = sum_t p[t, e]:
+ *   losses[0] = balance_coef / segments * sum_g E / (K T_g^2) sum_e c[g, e] P[g, e]     (1 per segment if even)
+ *   losses[1] = z_coef / sum_g T_g * sum_t (log sum_e exp(l[t, e]))^2
+ * Segments without a live token add nothing. */
+typedef struct moe_balance {
+  int32_t segments;   /* 1..4096, divides num_tokens */
+  float balance_coef;
+  float z_coef;
+} moe_balance_t;
+
+/* Bytes of device workspace of moe_balance_loss (0 for an invalid shape); its content does not matter. */
+size_t moe_balance_workspace_size(const moe_route_shape_t *shape, const moe_balance_t *balance);
+
+/*  in  logits, x_active_mask as for moe_route; topk_idx [T, K]: ids outside [0, E) are not counted
+ *  out losses [2] float32, counts [segments, E] int32, prob_sums [segments, E] float32, segment_tokens [segments] int32
+ *  workspace  16-byte aligned; calls that overlap need one each
+ * Of the shape, num_groups, topk_groups, group_score, renormalize and scale do not matter.  Sums of a few tokens' p in fp32,
+ * then in 64 bits, in an order that the sizes fix. */
+int moe_balance_loss(const moe_route_shape_t *shape, const moe_balance_t *balance, int32_t logits_fp32,
+                     const void *logits, const int32_t *topk_idx, const uint8_t *x_active_mask, float *losses,
+                     int32_t *counts, float *prob_sums, int32_t *segment_tokens, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Gradient of the logits through topk_weights and through both losses, in one pass.  The ids are taken as given
+ * (topk_idx [T, K]; slots outside [0, E) have no weight; an id that stands twice counts twice).  With the logarithms q_j of
+ * a token's scores at its ids, w_j its weights without the scale and d_j = grad_topk_weights[t, j]:
+ *   a_j = scale w_j (d_j - sum_i w_i d_i) with renormalize, else scale w_j d_j;
+ *   of the logarithms of the scores: sum over slots j with e of a_j  (softmax: - s_e sum_j a_j)
+ *     + p_e (A_e - sum_f p_f A_f), A_e = grad_losses[0] balance_coef E c[g, e] / (segments K T_g^2);
+ *   sigmoid: times 1 - s_e;   + grad_losses[1] z_coef 2 lse / (sum_g T_g) softmax(l)_e.
+ * Rows of tokens that are not live are zeros, and so are ids that have no logit.
+ *  balance            NULL: no losses, then counts, segment_tokens and grad_losses NULL as well
+ *  in  counts, segment_tokens from moe_balance_loss; grad_losses [2] float32 or NULL (ones)
+ *  in  grad_topk_weights [T, K] float32 or NULL (the losses alone); one of it and balance is needed.  With
+ *      dst_row ([T, K] from the layout; else NULL) it is moe_swiglu_grad's grad_row_weights instead: d_j =
+ *      grad_topk_weights[dst_row[t, j]], 0 for slots without a row
+ *  out grad_logits [T, E] of the logits' type, 16-byte aligned */
+int moe_route_grad(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
+                   const float *grad_topk_weights, const int32_t *dst_row, const uint8_t *x_active_mask,
+                   const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
+                   const float *grad_losses, void *grad_logits, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
