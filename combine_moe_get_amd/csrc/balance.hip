@@ -7,7 +7,7 @@ namespace moe {
 
 // Workgroups that share a segment's tokens.
 static int slices(int T, int S) {
-  const int n = T / S, most = (n + 15) / 16, want = (1024 + S - 1) / S;
+  const int n = T / S, most = (n + 31) / 32, want = (1024 + S - 1) / S;
   const int L = most < want ? most : want;
   return L < 1 ? 1 : L;
 }
@@ -42,94 +42,118 @@ static __host__ __device__ BalanceSpace balance_space(char *ws, int L, int E, in
 
 size_t balance_workspace(int T, int E, int S) { return balance_space(nullptr, slices(T, S), E, S).bytes; }
 
-// First kernel: a workgroup sums over a slice of a segment's tokens, a wave one token at a time.
-template <int NV, int SCORE, bool F32>
-__global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int L) {
-  __shared__ float red[4][64 * NV];
-  __shared__ int cnt[64 * NV];
-  __shared__ double zs[4];
-  __shared__ int lives[4];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int E = a.E, K = a.K, n = a.T / a.S, g = blockIdx.x / L, s = blockIdx.x - g * L;
-  const BalanceSpace ws = balance_space(a.ws, L, E, a.S);
+// First kernel: a workgroup sums over a slice of a segment's tokens.
+template <int L, int NV, int SCORE, bool F32>
+__global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int slices) {
+  constexpr int TOKENS = 4 * (64 / L);  // at a time
+  __shared__ __align__(16) float red[TOKENS][L * NV];
+  __shared__ int cnt[L * NV];
+  __shared__ double zs[TOKENS];
+  __shared__ int lives[TOKENS];
+  const int lane = threadIdx.x & (L - 1), sub = threadIdx.x / L;
+  const int E = a.E, K = a.K, n = a.T / a.S, g = blockIdx.x / slices, s = blockIdx.x - g * slices;
+  const BalanceSpace ws = balance_space(a.ws, slices, E, a.S);
   if (blockIdx.x == 0 && threadIdx.x == 0) *ws.counter = 0;
   for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
   __syncthreads();
-  const int64_t t0 = (int64_t)g * n + (int64_t)n * s / L, t1 = (int64_t)g * n + (int64_t)n * (s + 1) / L;
-  float acc[NV], p[NV], l[NV];
+  const int64_t t0 = (int64_t)g * n + (int64_t)n * s / slices, t1 = (int64_t)g * n + (int64_t)n * (s + 1) / slices;
+  float acc[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
   double z = 0.0;
   int live = 0;
-  for (int64_t t = t0 + wave; t < t1; t += 4) {
-    if (a.mask && !a.mask[t]) continue;
-    load_logits<NV, F32>(a.logits, t, E, lane, l);
-    const float m = row_max<NV>(l);
-    if (!(m > MOE_NEG_INF)) continue;
-    ++live;
-    probabilities<NV, SCORE>(l, m, p);
+  for (int64_t tb = t0; tb < t1; tb += TOKENS) {  // the same for all lanes of the wave
+    const int64_t t = tb + sub;
+    const bool on = t < t1 && (!a.mask || a.mask[t]);
+    float l[NV], p[NV], rest[NV];
+    load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
+    int id = on && lane < K ? a.idx[t * K + lane] : -1;
+    const float m = row_max<L, NV>(l);
+    const bool counts = m > MOE_NEG_INF;
+    scores<NV, SCORE>(l, m, p, rest);
+    float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] += p[i];
+    for (int i = 0; i < NV; ++i) sum += p[i];
+    sum = sum_of<L>(sum);
+    const float r = counts ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(p[i], r, acc[i]);
     if (a.z_coef != 0.0f) {
-      float sum = 0.0f;
+      if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+        sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += expf(l[i] - m);
-      const double lse = (double)m + log((double)wave_sum(sum));
+        for (int i = 0; i < NV; ++i) sum += l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+        sum = sum_of<L>(sum);
+      }
+      const double lse = counts ? (double)m + log((double)sum) : 0.0;
       z += lse * lse;
     }
-    const int id = lane < K ? a.idx[t * K + lane] : -1;
-    if (id >= 0 && id < E) atomicAdd(&cnt[id], 1);
+    live += counts;
+    if (counts && id >= 0 && id < E) atomicAdd(&cnt[id], 1);  // integers: in any order
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) red[wave][lane * NV + i] = acc[i];
+  for (int c = 0; c < NV / 4; ++c)
+    *(f32x4 *)&red[sub][id_of<L>(lane, c * 4)] = f32x4{acc[c * 4], acc[c * 4 + 1], acc[c * 4 + 2], acc[c * 4 + 3]};
   if (lane == 0) {
-    zs[wave] = z;
-    lives[wave] = live;
+    zs[sub] = z;
+    lives[sub] = live;
   }
   __syncthreads();
   const int64_t slot = (int64_t)blockIdx.x;
   for (int e = threadIdx.x; e < E; e += 256) {
-    ws.sum[slot * E + e] = (red[0][e] + red[1][e]) + (red[2][e] + red[3][e]);
+    float v = red[0][e];
+#pragma unroll
+    for (int k = 1; k < TOKENS; ++k) v += red[k][e];
+    ws.sum[slot * E + e] = v;
     ws.cnt[slot * E + e] = cnt[e];
   }
   if (threadIdx.x == 0) {
-    ws.z[slot] = (zs[0] + zs[1]) + (zs[2] + zs[3]);
-    ws.live[slot] = lives[0] + lives[1] + lives[2] + lives[3];
+    for (int k = 1; k < TOKENS; ++k) {
+      z += zs[k];
+      live += lives[k];
+    }
+    ws.z[slot] = z;
+    ws.live[slot] = live;
   }
 }
 
-// Second kernel: a workgroup 64 columns of a segment; the last one to finish adds the parts of the losses, in order.
-__global__ void __launch_bounds__(256) balance_losses_kernel(BalanceArgs a, int L) {
-  __shared__ double red[4][64];
-  __shared__ int redc[4][64];
+// Second kernel: a workgroup 64 columns of a segment, its waves every sixteenth slice; the last one to finish adds the parts
+// of the losses, in order.
+constexpr int kWaves = 16;
+__global__ void __launch_bounds__(64 * kWaves) balance_losses_kernel(BalanceArgs a, int slices) {
+  __shared__ double red[kWaves][64];
+  __shared__ int redc[kWaves][64];
   __shared__ int last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.E, nb = (E + 63) / 64, g = blockIdx.x / nb, e = (blockIdx.x - g * nb) * 64 + lane;
-  const BalanceSpace ws = balance_space(a.ws, L, E, a.S);
+  const BalanceSpace ws = balance_space(a.ws, slices, E, a.S);
   double sum = 0.0;
-  int cnt = 0;
+  int cnt = 0, n = 0;
   if (e < E) {
-    for (int s = wave; s < L; s += 4) {
-      sum += (double)ws.sum[((int64_t)g * L + s) * E + e];
-      cnt += ws.cnt[((int64_t)g * L + s) * E + e];
+#pragma unroll 4
+    for (int s = wave; s < slices; s += kWaves) {
+      sum += (double)ws.sum[((int64_t)g * slices + s) * E + e];
+      cnt += ws.cnt[((int64_t)g * slices + s) * E + e];
     }
   }
+  if (wave == 0)
+    for (int s = lane; s < slices; s += 64) n += ws.live[(int64_t)g * slices + s];
   red[wave][lane] = sum;
   redc[wave][lane] = cnt;
   __syncthreads();
   if (wave == 0) {
-    int n = 0;
-    for (int s = lane; s < L; s += 64) n += ws.live[(int64_t)g * L + s];
-    n = readlane(wave_inclusive_sum(n), 63);
-    sum = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
-    cnt = redc[0][lane] + redc[1][lane] + redc[2][lane] + redc[3][lane];
+    n = sum_of<64>(n);
+    for (int v = 1; v < kWaves; ++v) {
+      sum += red[v][lane];
+      cnt += redc[v][lane];
+    }
     if (e < E) {
       a.counts[(int64_t)g * E + e] = cnt;
       a.sums[(int64_t)g * E + e] = (float)sum;
     }
-    if (lane == 0 && e == 0) a.tokens[g] = n;
+    if (e == 0) a.tokens[g] = n;
     const double f = n > 0 ? (double)a.balance_coef * E / ((double)a.S * a.K * n * n) : 0.0;
-    const double part = wave_sum(f * cnt * sum);
+    const double part = sum_of<64>(f * cnt * sum);
     if (lane == 0) {
       __hip_atomic_store(&ws.part[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       last = __hip_atomic_fetch_add(ws.counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
@@ -138,16 +162,16 @@ __global__ void __launch_bounds__(256) balance_losses_kernel(BalanceArgs a, int 
   __syncthreads();
   if (!last) return;
   double loss = 0.0, z = 0.0;
-  int n = 0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 256)
+  n = 0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += 64 * kWaves)
     loss += __hip_atomic_load(&ws.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = threadIdx.x; i < a.S * L; i += 256) {
+  for (int i = threadIdx.x; i < a.S * slices; i += 64 * kWaves) {
     z += ws.z[i];
     n += ws.live[i];
   }
-  loss = wave_sum(loss);
-  z = wave_sum(z);
-  n = readlane(wave_inclusive_sum(n), 63);
+  loss = sum_of<64>(loss);
+  z = sum_of<64>(z);
+  n = sum_of<64>(n);
   if (lane == 0) {
     red[wave][0] = loss;
     red[wave][1] = z;
@@ -155,7 +179,7 @@ __global__ void __launch_bounds__(256) balance_losses_kernel(BalanceArgs a, int 
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int v = 1; v < 4; ++v) {
+    for (int v = 1; v < kWaves; ++v) {
       loss += red[v][0];
       z += red[v][1];
       n += redc[v][0];
@@ -165,171 +189,204 @@ __global__ void __launch_bounds__(256) balance_losses_kernel(BalanceArgs a, int 
   }
 }
 
+// f(score, whether fp32) with both as constants
+template <class F>
+static void with_types(int score, bool fp32, F &&f) {
+  using Soft = std::integral_constant<int, MOE_SCORE_SOFTMAX>;
+  using Sig = std::integral_constant<int, MOE_SCORE_SIGMOID>;
+  if (score == MOE_SCORE_SOFTMAX && fp32) f(Soft{}, std::true_type{});
+  else if (score == MOE_SCORE_SOFTMAX) f(Soft{}, std::false_type{});
+  else if (fp32) f(Sig{}, std::true_type{});
+  else f(Sig{}, std::false_type{});
+}
+
 hipError_t launch_balance(const BalanceArgs &a, int score, bool fp32, hipStream_t st) {
-  const int L = slices(a.T, a.S);
-  with_values(a.E, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
-    auto go = [&](auto sc, auto f32) {
-      hipLaunchKernelGGL((balance_sums_kernel<NV, decltype(sc)::value, decltype(f32)::value>), dim3((unsigned)(a.S * L)),
-                         dim3(256), 0, st, a, L);
-    };
-    if (score == MOE_SCORE_SOFTMAX) {
-      if (fp32) go(std::integral_constant<int, MOE_SCORE_SOFTMAX>{}, std::true_type{});
-      else go(std::integral_constant<int, MOE_SCORE_SOFTMAX>{}, std::false_type{});
-    } else {
-      if (fp32) go(std::integral_constant<int, MOE_SCORE_SIGMOID>{}, std::true_type{});
-      else go(std::integral_constant<int, MOE_SCORE_SIGMOID>{}, std::false_type{});
-    }
+  const int n = slices(a.T, a.S);
+  with_token(a.E, [&](auto tok) {
+    constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES;
+    with_types(score, fp32, [&](auto sc, auto f32) {
+      hipLaunchKernelGGL((balance_sums_kernel<L, NV, decltype(sc)::value, decltype(f32)::value>), dim3((unsigned)(a.S * n)),
+                         dim3(256), 0, st, a, n);
+    });
   });
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_losses_kernel, dim3((unsigned)(a.S * ((a.E + 63) / 64))), dim3(256), 0, st, a, L);
+  hipLaunchKernelGGL(balance_losses_kernel, dim3((unsigned)(a.S * ((a.E + 63) / 64))), dim3(64 * kWaves), 0, st, a, n);
   return hipGetLastError();
 }
 
 // ---- the gradient --------------------------------------------------------------------------------
 
-template <int NV, bool F32>
+template <int L, int NV, bool F32>
 __device__ __forceinline__ void store_grad(void *out, int64_t t, int E, int lane, const float *d) {
-  typedef __bf16 b16;
-  const int e0 = lane * NV;
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  const bool wide = (E & 3) == 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (e0 + i < E) {
-      if constexpr (F32) ((float *)out)[t * E + e0 + i] = d[i];
-      else ((b16 *)out)[t * E + e0 + i] = (b16)d[i];  // to nearest even
+  for (int c = 0; c < NV / 4; ++c) {
+    const int e = id_of<L>(lane, c * 4);
+    const float *v = d + c * 4;
+    const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};  // to nearest even
+    if (wide) {
+      if (e < E) {
+        if constexpr (F32) *(f32x4 *)((float *)out + t * E + e) = f32x4{v[0], v[1], v[2], v[3]};
+        else *(bf16x4 *)((__bf16 *)out + t * E + e) = h;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (e + k < E) {
+          if constexpr (F32) ((float *)out)[t * E + e + k] = v[k];
+          else ((__bf16 *)out)[t * E + e + k] = h[k];
+        }
     }
   }
 }
 
-template <int NV, int SCORE, bool F32>
+template <int L, int NV, int SCORE, bool F32>
 __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
+  constexpr int TOKENS = 4 * (64 / L);
+  __shared__ __align__(16) float rows[TOKENS][L * NV];  // what goes to a token's chosen ids
   __shared__ int parts[4];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & (L - 1), sub = threadIdx.x / L;
   const int E = a.E, K = a.K;
   const bool losses = a.counts != nullptr, zloss = losses && a.z_coef != 0.0f;
-  double per_token = 0.0;  // of the z loss
+  const float per_balance = losses ? (float)((double)(a.gl ? a.gl[0] : 1.0f) * a.balance_coef * E / ((double)a.S * K)) : 0.0f;
+  float per_z = 0.0f;  // of a token
   if (zloss) {
     int n = 0;
     for (int i = threadIdx.x; i < a.S; i += 256) n += a.tokens[i];
-    n = wave_inclusive_sum(n);
-    if (lane == 63) parts[wave] = n;
+    n = sum_of<64>(n);
+    if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = n;
     __syncthreads();
     n = parts[0] + parts[1] + parts[2] + parts[3];
-    per_token = n > 0 ? 2.0 * a.z_coef * (a.gl ? a.gl[1] : 1.0f) / n : 0.0;
+    per_z = n > 0 ? (float)(2.0 * a.z_coef * (a.gl ? a.gl[1] : 1.0f) / n) : 0.0f;
   }
-  const int n = losses ? a.T / a.S : 1;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < a.T; t += (int64_t)gridDim.x * 4) {
-    float l[NV], p[NV], d[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) d[i] = 0.0f;
-    float m = MOE_NEG_INF;
-    if (!a.mask || a.mask[t]) {
-      load_logits<NV, F32>(a.logits, t, E, lane, l);
-      m = row_max<NV>(l);
+  const uint32_t n = losses ? (uint32_t)(a.T / a.S) : 1;
+  for (int64_t tb = (int64_t)blockIdx.x * TOKENS; tb < a.T; tb += (int64_t)gridDim.x * TOKENS) {
+    const int64_t t = tb + sub;
+    const bool on = t < a.T && (!a.mask || a.mask[t]);
+    float l[NV], p[NV], rest[NV], d[NV];
+    load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
+    int id = on && a.gw && lane < K ? a.idx[t * K + lane] : -1;
+    if (id < 0 || id >= E) id = -1;
+    float lj = MOE_NEG_INF, gw = 0.0f;
+    if (id >= 0) {
+      lj = logit_at(a.logits, F32, t * E + id);
+      const int64_t at = t * K + lane;
+      if (!a.dst) {
+        gw = a.gw[at];
+      } else {
+        const int r = a.dst[at];
+        if (r >= 0) gw = a.gw[r];
+      }
     }
-    if (m > MOE_NEG_INF) {
-      probabilities<NV, SCORE>(l, m, p);
-      float sum_a = 0.0f, aj = 0.0f;
-      int id = -1;
-      if (a.gw) {
-        if (lane < K) id = a.idx[t * K + lane];
-        if (id >= E) id = -1;
-        const float lj = id >= 0 ? logit_at(a.logits, F32, t * E + id) : MOE_NEG_INF;
-        const bool some = lj > MOE_NEG_INF;
-        float gw = 0.0f;
-        if (some) {
-          if (!a.dst) {
-            gw = a.gw[t * K + lane];
-          } else {
-            const int r = a.dst[t * K + lane];
-            if (r >= 0) gw = a.gw[r];
-          }
-        }
-        if (a.renorm) {
-          const float q = !some ? MOE_NEG_INF : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
-          const float mq = wave_max(q);
-          const float e = some ? expf(q - mq) : 0.0f;
-          const float sum = wave_sum(e);  // by every lane, as all such sums
-          const float w = some ? e / sum : 0.0f;
-          const float mean = wave_sum(w * gw);
-          aj = some ? a.scale * w * (gw - mean) : 0.0f;
-        } else {
-          float s;
-          if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-            float sum = 0.0f;
+    const bool some = lj > MOE_NEG_INF;
+    if (!some) gw = 0.0f;
+    const float m = row_max<L, NV>(l);
+    const bool counts = m > MOE_NEG_INF;
+    scores<NV, SCORE>(l, m, p, rest);
+    float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) sum += expf(l[i] - m);
-            sum = wave_sum(sum);
-            s = expf(lj - m) / sum;
-          } else {
-            s = 1.0f / (1.0f + expf(-lj));
-          }
-          aj = some ? a.scale * s * gw : 0.0f;
-          if (SCORE == MOE_SCORE_SOFTMAX) sum_a = wave_sum(aj);
-        }
-        for (int j = 0; j < K; ++j) {
-          const int e = readlane(id, j) - lane * NV;
-          const float v = readlane_f(aj, j);
+    for (int i = 0; i < NV; ++i) sum += p[i];
+    sum = sum_of<L>(sum);
+    const float r = counts ? 1.0f / sum : 0.0f;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) d[i] += e == i ? v : 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] -= sum_a * p[i];
+    for (int i = 0; i < NV; ++i) {
+      p[i] *= r;
+      d[i] = 0.0f;
+    }
+    if (a.gw) {
+      // of the logarithms of the scores of the token's ids: slot j on lane j
+      float aj, sum_a = 0.0f;
+      if (a.renorm) {
+        const float q = !some ? MOE_NEG_INF : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
+        const float mq = max_of<L>(q);
+        float w = some ? exp_neg(q - mq) : 0.0f;
+        const float all = sum_of<L>(w);
+        w = some ? w / all : 0.0f;
+        const float mean = sum_of<L>(w * gw);
+        aj = a.scale * w * (gw - mean);
+      } else {
+        const float s = !some ? 0.0f : SCORE == MOE_SCORE_SOFTMAX ? exp_neg(lj - m) * r : 1.0f / (1.0f + expf(-lj));
+        aj = a.scale * s * gw;
+        if (SCORE == MOE_SCORE_SOFTMAX) sum_a = sum_of<L>(aj);
       }
-      if (losses) {
-        const int64_t g = t / n;
-        const int live = a.tokens[g];
-        const float f = live > 0 ? (float)((double)(a.gl ? a.gl[0] : 1.0f) * a.balance_coef * E / ((double)a.S * K * live * live)) : 0.0f;
-        const float c0 = (float)((double)K * live / E);  // sum p = 1: any constant may be taken off; the mean loses least
-        float A[NV], s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = lane * NV + i;
-          A[i] = e < E ? f * ((float)a.counts[g * E + e] - c0) : 0.0f;
-          s += A[i] * p[i];
-        }
-        s = wave_sum(s);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] += p[i] * (A[i] - s);
+      // to the lanes that hold the ids, through LDS; slots of the same id all carry their sum
+      float whole = 0.0f;
+      for (int j = 0; j < K; ++j) {
+        const int o = __shfl(id, j, L);
+        const float v = __shfl(aj, j, L);
+        whole += o == id ? v : 0.0f;
       }
+#pragma unroll
+      for (int c = 0; c < NV / 4; ++c) *(f32x4 *)&rows[sub][id_of<L>(lane, c * 4)] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (id >= 0) rows[sub][id] = whole;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int c = 0; c < NV / 4; ++c) {
+        const f32x4 v = *(const f32x4 *)&rows[sub][id_of<L>(lane, c * 4)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) d[c * 4 + k] = __builtin_fmaf(-sum_a, p[c * 4 + k], v[k]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if (losses) {
+      const uint32_t g = on ? (uint32_t)t / n : 0;
+      const int live = a.tokens[g];
+      const float f = live > 0 ? per_balance / (float)live / (float)live : 0.0f;
+      const float c0 = (float)K * (float)live / (float)E;  // sum p = 1: any constant may be taken off; the mean loses least
+      float A[NV], s = 0.0f;
+      const int32_t *ct = a.counts + (int64_t)g * E;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = id_of<L>(lane, i);
+        A[i] = e < E ? f * ((float)ct[e] - c0) : 0.0f;
+        s = __builtin_fmaf(A[i], p[i], s);
+      }
+      s = sum_of<L>(s);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(p[i], A[i] - s, d[i]);
+    }
+    if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] *= rest[i];
+    }
+    if (zloss) {
+      float e[NV];
       if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] *= 1.0f / (1.0f + expf(l[i]));
-      }
-      if (zloss) {
-        float e[NV], sum = 0.0f;
+        sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          e[i] = expf(l[i] - m);
+          e[i] = l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
           sum += e[i];
         }
-        sum = wave_sum(sum);
-        const float f = (float)(per_token * ((double)m + log((double)sum)) / sum);
+        sum = sum_of<L>(sum);
+      }
+      const float lse = counts ? m + logf(sum) : 0.0f;
+      const float f = counts ? per_z * lse : 0.0f;
+      if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+        const float fr = counts ? f / sum : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] += f * e[i];
+        for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(fr, e[i], d[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(f, p[i], d[i]);
       }
     }
-    store_grad<NV, F32>(a.out, t, E, lane, d);
+    if (t < a.T) store_grad<L, NV, F32>(a.out, t, E, lane, d);
   }
 }
 
 hipError_t launch_route_grad(const RouteGradArgs &a, int score, bool fp32, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  const int wg = (a.T + 3) / 4;
-  const dim3 grid((unsigned)(wg < 2048 ? wg : 2048)), block(256);
-  with_values(a.E, [&](auto nv) {
-    constexpr int NV = decltype(nv)::value;
-    auto go = [&](auto sc, auto f32) {
-      hipLaunchKernelGGL((route_grad_kernel<NV, decltype(sc)::value, decltype(f32)::value>), grid, block, 0, st, a);
-    };
-    if (score == MOE_SCORE_SOFTMAX) {
-      if (fp32) go(std::integral_constant<int, MOE_SCORE_SOFTMAX>{}, std::true_type{});
-      else go(std::integral_constant<int, MOE_SCORE_SOFTMAX>{}, std::false_type{});
-    } else {
-      if (fp32) go(std::integral_constant<int, MOE_SCORE_SIGMOID>{}, std::true_type{});
-      else go(std::integral_constant<int, MOE_SCORE_SIGMOID>{}, std::false_type{});
-    }
+  with_token(a.E, [&](auto tok) {
+    constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES, TOKENS = 4 * (64 / L);
+    const int wg = (a.T + TOKENS - 1) / TOKENS;
+    with_types(score, fp32, [&](auto sc, auto f32) {
+      hipLaunchKernelGGL((route_grad_kernel<L, NV, decltype(sc)::value, decltype(f32)::value>),
+                         dim3((unsigned)(wg < 4096 ? wg : 4096)), dim3(256), 0, st, a);
+    });
   });
   return hipGetLastError();
 }

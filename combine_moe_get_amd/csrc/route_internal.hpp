@@ -17,6 +17,7 @@ struct RouteArgs {
   int32_t T, E, K, G, keep;
   int32_t two, renorm;
   float scale;
+  uint32_t div_per;      // div_magic of the ids of a group; set by the launcher
 };
 hipError_t launch_route(const RouteArgs &a, int score, bool fp32, hipStream_t stream);
 
@@ -52,41 +53,63 @@ hipError_t launch_route_grad(const RouteGradArgs &a, int score, bool fp32, hipSt
 
 #define MOE_NEG_INF (-__builtin_inff())
 
-// a DPP move of a value of 4 or 8 bytes; lanes without a source take `old`
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ float dpp(float old, float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROW_MASK, 0xf, false));
-}
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ double dpp(double old, double v) {
-  const int lo = __builtin_amdgcn_update_dpp(__double2loint(old), __double2loint(v), CTRL, ROW_MASK, 0xf, false);
-  const int hi = __builtin_amdgcn_update_dpp(__double2hiint(old), __double2hiint(v), CTRL, ROW_MASK, 0xf, false);
-  return __hiloint2double(hi, lo);
-}
-__device__ __forceinline__ float lane_value(float v, int lane) { return readlane_f(v, lane); }
-__device__ __forceinline__ double lane_value(double v, int lane) {
-  return __hiloint2double(readlane(__double2hiint(v), lane), readlane(__double2loint(v), lane));
+// ---- a token on L lanes of a wave (16, 32 or 64), 64 / L tokens a wave --------------------------------
+//
+// A lane holds NV of its token's logits, four neighbouring ids at a time: value i is of id (i / 4 * L + lane) * 4 + i % 4.
+// Sixteen lanes are a DPP row, whose folds need no LDS; and what a wave does once it does for four tokens: the K best of
+// 256 ids of 16384 tokens took 9 us on 64 lanes a token, XX on 16.
+template <int L, int NV>
+struct Token {
+  static constexpr int LANES = L, VALUES = NV;
+};
+
+// f(Token) for the least that holds E ids
+template <class F>
+inline void with_token(int E, F &&f) {
+  if (E <= 64) f(Token<16, 4>{});
+  else if (E <= 128) f(Token<16, 8>{});
+  else if (E <= 256) f(Token<16, 16>{});
+  else if (E <= 512) f(Token<32, 16>{});
+  else if (E <= 1024) f(Token<64, 16>{});
+  else f(Token<64, 32>{});
 }
 
-// max and sum over the 64 lanes, to every lane (see wave_max, wave_inclusive_sum); in a fixed order
-__device__ __forceinline__ double wave_max(double v) {
-  v = fmax(v, dpp<0x111, 0xf>(v, v));
-  v = fmax(v, dpp<0x112, 0xf>(v, v));
-  v = fmax(v, dpp<0x114, 0xf>(v, v));
-  v = fmax(v, dpp<0x118, 0xf>(v, v));
-  v = fmax(v, dpp<0x142, 0xa>(v, v));
-  v = fmax(v, dpp<0x143, 0xc>(v, v));
-  return lane_value(v, 63);
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
 }
-template <class F>
-__device__ __forceinline__ F wave_sum(F v) {
-  v += dpp<0x111, 0xf>(F(0), v);
-  v += dpp<0x112, 0xf>(F(0), v);
-  v += dpp<0x114, 0xf>(F(0), v);
-  v += dpp<0x118, 0xf>(F(0), v);
-  v += dpp<0x142, 0xa>(F(0), v);
-  v += dpp<0x143, 0xc>(F(0), v);
-  return lane_value(v, 63);
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf, 0xf, false),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf, 0xf, false));
+}
+
+// op over the L lanes of a token, to each of them, in a fixed order.  Every lane of the wave must call it.
+template <int L, class V, class Op>
+__device__ __forceinline__ V fold(V v, Op op) {
+  v = op(v, dpp<0xb1>(v));   // quad_perm 1 0 3 2
+  v = op(v, dpp<0x4e>(v));   // quad_perm 2 3 0 1
+  v = op(v, dpp<0x141>(v));  // row_half_mirror
+  v = op(v, dpp<0x140>(v));  // row_mirror
+  if constexpr (L > 16) v = op(v, __shfl_xor(v, 16));
+  if constexpr (L > 32) v = op(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  return fold<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ __forceinline__ double max_of(double v) {
+  return fold<L>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int L, class V>
+__device__ __forceinline__ V sum_of(V v) {
+  return fold<L>(v, [](V a, V b) { return a + b; });
 }
 
 // a logit that counts: +inf as the largest finite value, NaN as -inf
@@ -96,91 +119,87 @@ __device__ __forceinline__ float logit_at(const void *logits, bool fp32, int64_t
   return usable(fp32 ? ((const float *)logits)[i] : __uint_as_float((uint32_t)((const uint16_t *)logits)[i] << 16));
 }
 
-// a lane's NV consecutive logits lane * NV, .. of the token's E; -inf behind the last.  Wide loads where rows begin at
-// multiples of NV.
-template <int NV, bool F32>
-__device__ __forceinline__ void load_logits(const void *logits, int64_t t, int E, int lane, float *l) {
-  const int e0 = lane * NV;
-  if (E % NV == 0) {
-    if (e0 < E) {
-      if constexpr (F32) {
-        constexpr int B = NV < 4 ? NV : 4;
-        typedef float vec __attribute__((ext_vector_type(B)));
-        const float *p = (const float *)logits + t * E + e0;
-#pragma unroll
-        for (int i = 0; i < NV; i += B) {
-          if constexpr (B == 1) l[i] = p[i];
-          else {
-            const vec v = *(const vec *)(p + i);
-#pragma unroll
-            for (int k = 0; k < B; ++k) l[i + k] = v[k];
-          }
-        }
-      } else {
-        constexpr int B = NV < 8 ? NV : 8;
-        typedef uint16_t vec __attribute__((ext_vector_type(B)));
-        const uint16_t *p = (const uint16_t *)logits + t * E + e0;
-#pragma unroll
-        for (int i = 0; i < NV; i += B) {
-          if constexpr (B == 1) l[i] = __uint_as_float((uint32_t)p[i] << 16);
-          else {
-            const vec v = *(const vec *)(p + i);
-#pragma unroll
-            for (int k = 0; k < B; ++k) l[i + k] = __uint_as_float((uint32_t)v[k] << 16);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) l[i] = usable(l[i]);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) l[i] = MOE_NEG_INF;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) l[i] = e0 + i < E ? logit_at(logits, F32, t * E + e0 + i) : MOE_NEG_INF;
+// the id of a lane's value i
+template <int L>
+__device__ __forceinline__ int id_of(int lane, int i) {
+  return ((i >> 2) * L + lane) * 4 + (i & 3);
 }
 
-// the largest of a token's logits, to every lane
-template <int NV>
+// A lane's logits of token t; -inf where there is none (`on`: whether the token counts).  Rows of a multiple of four ids are
+// read four at a time.
+template <int L, int NV, bool F32>
+__device__ __forceinline__ void load_logits(const void *logits, int64_t t, int E, int lane, bool on, float *l) {
+  const bool wide = (E & 3) == 0;
+#pragma unroll
+  for (int c = 0; c < NV / 4; ++c) {
+    const int e = id_of<L>(lane, c * 4);
+    float *v = l + c * 4;
+    v[0] = v[1] = v[2] = v[3] = MOE_NEG_INF;
+    if (wide) {
+      if (on && e < E) {
+        if constexpr (F32) {
+          const f32x4 x = *(const f32x4 *)((const float *)logits + t * E + e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = x[k];
+        } else {
+          const u32x2 x = *(const u32x2 *)((const uint16_t *)logits + t * E + e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (on && e + k < E) {
+          if constexpr (F32) v[k] = ((const float *)logits)[t * E + e + k];
+          else v[k] = __uint_as_float((uint32_t)((const uint16_t *)logits)[t * E + e + k] << 16);
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l[i] = usable(l[i]);
+}
+
+template <int L, int NV>
 __device__ __forceinline__ float row_max(const float *l) {
   float m = l[0];
 #pragma unroll
   for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-  return wave_max(m);
+  return max_of<L>(m);
 }
 
-// p = scores of the logits divided by their sum, for a token with a logit; m: the largest logit.  Softmax: exp(l - m).
-// Sigmoid: exp(min(l, 0)) / (1 + exp(-|l|)); where all of them are small, both divided by exp(m), so that none vanishes.
+// exp(x) for x <= 0 (-inf and below -200: 0), good to some two steps of fp32: 2^t of t = x log2(e) rounded, and the rest of
+// the product as a factor
+__device__ __forceinline__ float exp_neg(float x) {
+  const float c = fmaxf(x, -200.0f);
+  const float t = c * 1.44269502e+00f;
+  const float r = __builtin_fmaf(c, 1.92596299e-8f, __builtin_fmaf(c, 1.44269502e+00f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e * 0.693147182f, r, e);
+}
+
+// The scores of a token's logits up to a common factor, s, and for sigmoids 1 - sigmoid, rest.  m: its largest logit.
+// Softmax: exp(l - m).  Sigmoid: with e = exp(-|l|), e / (1 + e) or 1 / (1 + e); of a token with no logit above -60 divided
+// by exp(m), so that they do not vanish.  0 where there is no logit.
 template <int NV, int SCORE>
-__device__ __forceinline__ void probabilities(const float *l, float m, float *p) {
-  float sum = 0.0f;
-  const float shift = SCORE == MOE_SCORE_SOFTMAX ? m : fminf(m, 0.0f);
+__device__ __forceinline__ void scores(const float *l, float m, float *s, float *rest) {
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if constexpr (SCORE == MOE_SCORE_SOFTMAX) p[i] = expf(l[i] - shift);
-    else p[i] = expf(fminf(l[i], 0.0f) - shift) / (1.0f + expf(-fabsf(l[i])));
-    if (!(l[i] > MOE_NEG_INF)) p[i] = 0.0f;
-    sum += p[i];
+    for (int i = 0; i < NV; ++i) s[i] = l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+  } else {
+    const bool low = m < -60.0f;
+    const float shift = low ? m : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float e = exp_neg(-fabsf(l[i] - shift)), r = low ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e);
+      s[i] = l[i] > 0.0f ? r : e * r;
+      rest[i] = l[i] > 0.0f ? e * r : r;
+      if (!(l[i] > MOE_NEG_INF)) s[i] = rest[i] = 0.0f;
+    }
   }
-  const float r = 1.0f / wave_sum(sum);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) p[i] *= r;
 }
 
 // the logarithm of a sigmoid
 __device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
-
-// kernels are built for rows of up to 64 NV logits: f(NV) for the least NV that holds E
-template <class F>
-inline void with_values(int E, F &&f) {
-  if (E <= 64) f(std::integral_constant<int, 1>{});
-  else if (E <= 128) f(std::integral_constant<int, 2>{});
-  else if (E <= 256) f(std::integral_constant<int, 4>{});
-  else if (E <= 512) f(std::integral_constant<int, 8>{});
-  else if (E <= 1024) f(std::integral_constant<int, 16>{});
-  else f(std::integral_constant<int, 32>{});
-}
 
 }  // namespace moe
