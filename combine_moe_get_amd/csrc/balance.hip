@@ -42,6 +42,17 @@ static __host__ __device__ BalanceSpace balance_space(char *ws, int L, int E, in
 
 size_t balance_workspace(int T, int E, int S) { return balance_space(nullptr, slices(T, S), E, S).bytes; }
 
+// As with_token: here all four tokens of a wave pay at any number (4096 of 256 ids: 12.2 us on 16 lanes, 13.6 on 32).
+template <class F>
+static void with_sums_token(int E, F &&f) {
+  if (E <= 64) f(Token<16, 4>{});
+  else if (E <= 128) f(Token<16, 8>{});
+  else if (E <= 256) f(Token<16, 16>{});
+  else if (E <= 512) f(Token<32, 16>{});
+  else if (E <= 1024) f(Token<64, 16>{});
+  else f(Token<64, 32>{});
+}
+
 // First kernel: a workgroup sums over a slice of a segment's tokens.
 template <int L, int NV, int SCORE, bool F32>
 __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int slices) {
@@ -117,35 +128,38 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
   }
 }
 
-// Second kernel: a workgroup 64 columns of a segment, its waves every sixteenth slice; the last one to finish adds the parts
-// of the losses, in order.
-constexpr int kWaves = 16;
-__global__ void __launch_bounds__(64 * kWaves) balance_losses_kernel(BalanceArgs a, int slices) {
-  __shared__ double red[kWaves][64];
-  __shared__ int redc[kWaves][64];
+// Second kernel: a workgroup C columns of a segment, 1024 / C parts of its slices; the last one to finish adds the parts of
+// the losses, in order.
+template <int C>
+__global__ void __launch_bounds__(1024) balance_losses_kernel(BalanceArgs a, int slices) {
+  constexpr int PARTS = 1024 / C;
+  __shared__ double red[PARTS][C];
+  __shared__ int redc[PARTS][C];
+  __shared__ double reds[16];
   __shared__ int last;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int E = a.E, nb = (E + 63) / 64, g = blockIdx.x / nb, e = (blockIdx.x - g * nb) * 64 + lane;
+  const int tid = threadIdx.x, col = tid & (C - 1), part = tid / C;
+  const int E = a.E, nb = (E + C - 1) / C, g = blockIdx.x / nb, e = (blockIdx.x - g * nb) * C + col;
   const BalanceSpace ws = balance_space(a.ws, slices, E, a.S);
   double sum = 0.0;
   int cnt = 0, n = 0;
   if (e < E) {
 #pragma unroll 4
-    for (int s = wave; s < slices; s += kWaves) {
+    for (int s = part; s < slices; s += PARTS) {
       sum += (double)ws.sum[((int64_t)g * slices + s) * E + e];
       cnt += ws.cnt[((int64_t)g * slices + s) * E + e];
     }
   }
-  if (wave == 0)
-    for (int s = lane; s < slices; s += 64) n += ws.live[(int64_t)g * slices + s];
-  red[wave][lane] = sum;
-  redc[wave][lane] = cnt;
+  red[part][col] = sum;
+  redc[part][col] = cnt;
+  if (part == 0)  // by each of its waves
+    for (int s = tid & 63; s < slices; s += 64) n += ws.live[(int64_t)g * slices + s];
   __syncthreads();
-  if (wave == 0) {
+  if (part == 0) {
     n = sum_of<64>(n);
-    for (int v = 1; v < kWaves; ++v) {
-      sum += red[v][lane];
-      cnt += redc[v][lane];
+#pragma unroll
+    for (int v = 1; v < PARTS; ++v) {
+      sum += red[v][col];
+      cnt += redc[v][col];
     }
     if (e < E) {
       a.counts[(int64_t)g * E + e] = cnt;
@@ -153,36 +167,44 @@ __global__ void __launch_bounds__(64 * kWaves) balance_losses_kernel(BalanceArgs
     }
     if (e == 0) a.tokens[g] = n;
     const double f = n > 0 ? (double)a.balance_coef * E / ((double)a.S * a.K * n * n) : 0.0;
-    const double part = sum_of<64>(f * cnt * sum);
-    if (lane == 0) {
-      __hip_atomic_store(&ws.part[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(ws.counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-    }
+    const double mine = sum_of<64>(f * cnt * sum);
+    if ((tid & 63) == 0) reds[tid >> 6] = mine;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double mine = reds[0];
+    for (int v = 1; v < C / 64; ++v) mine += reds[v];
+    // the part is in memory, past this XCD's caches, before the count says so
+    __hip_atomic_store(&ws.part[blockIdx.x], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    last = __hip_atomic_fetch_add(ws.counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   double loss = 0.0, z = 0.0;
   n = 0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += 64 * kWaves)
+  for (int i = tid; i < (int)gridDim.x; i += 1024)
     loss += __hip_atomic_load(&ws.part[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  for (int i = threadIdx.x; i < a.S * slices; i += 64 * kWaves) {
+  for (int i = tid; i < a.S * slices; i += 1024) {
     z += ws.z[i];
     n += ws.live[i];
   }
   loss = sum_of<64>(loss);
   z = sum_of<64>(z);
   n = sum_of<64>(n);
-  if (lane == 0) {
-    red[wave][0] = loss;
-    red[wave][1] = z;
-    redc[wave][0] = n;
+  double *lr = &red[0][0], *zr = lr + 16;
+  int *nr = &redc[0][0];
+  if ((tid & 63) == 0) {
+    lr[tid >> 6] = loss;
+    zr[tid >> 6] = z;
+    nr[tid >> 6] = n;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int v = 1; v < kWaves; ++v) {
-      loss += red[v][0];
-      z += red[v][1];
-      n += redc[v][0];
+  if (tid == 0) {
+    for (int v = 1; v < 16; ++v) {
+      loss += lr[v];
+      z += zr[v];
+      n += nr[v];
     }
     a.losses[0] = (float)loss;
     a.losses[1] = n > 0 ? (float)((double)a.z_coef * z / n) : 0.0f;
@@ -202,7 +224,7 @@ static void with_types(int score, bool fp32, F &&f) {
 
 hipError_t launch_balance(const BalanceArgs &a, int score, bool fp32, hipStream_t st) {
   const int n = slices(a.T, a.S);
-  with_token(a.E, [&](auto tok) {
+  with_sums_token(a.E, [&](auto tok) {
     constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES;
     with_types(score, fp32, [&](auto sc, auto f32) {
       hipLaunchKernelGGL((balance_sums_kernel<L, NV, decltype(sc)::value, decltype(f32)::value>), dim3((unsigned)(a.S * n)),
@@ -211,7 +233,8 @@ hipError_t launch_balance(const BalanceArgs &a, int score, bool fp32, hipStream_
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_losses_kernel, dim3((unsigned)(a.S * ((a.E + 63) / 64))), dim3(64 * kWaves), 0, st, a, n);
+  if (n >= 16) hipLaunchKernelGGL((balance_losses_kernel<64>), dim3((unsigned)(a.S * ((a.E + 63) / 64))), dim3(1024), 0, st, a, n);
+  else hipLaunchKernelGGL((balance_losses_kernel<256>), dim3((unsigned)(a.S * ((a.E + 255) / 256))), dim3(1024), 0, st, a, n);
   return hipGetLastError();
 }
 
@@ -312,24 +335,30 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
         if (SCORE == MOE_SCORE_SOFTMAX) sum_a = sum_of<L>(aj);
       }
       // to the lanes that hold the ids, through LDS; slots of the same id all carry their sum
-      float whole = 0.0f;
-      for (int j = 0; j < K; ++j) {
-        const int o = __shfl(id, j, L);
-        const float v = __shfl(aj, j, L);
-        whole += o == id ? v : 0.0f;
+      float whole = aj;
+      if (id >= 0) rows[sub][id] = __int_as_float(lane);
+      lds_order();
+      if (ballot(id >= 0 && __float_as_int(rows[sub][id >= 0 ? id : 0]) != lane)) {
+        whole = 0.0f;
+        for (int j = 0; j < K; ++j) {
+          const int o = __shfl(id, j, L);
+          const float v = __shfl(aj, j, L);
+          whole += o == id ? v : 0.0f;
+        }
       }
+      lds_order();
 #pragma unroll
       for (int c = 0; c < NV / 4; ++c) *(f32x4 *)&rows[sub][id_of<L>(lane, c * 4)] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      lds_order();
       if (id >= 0) rows[sub][id] = whole;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      lds_order();
 #pragma unroll
       for (int c = 0; c < NV / 4; ++c) {
         const f32x4 v = *(const f32x4 *)&rows[sub][id_of<L>(lane, c * 4)];
 #pragma unroll
         for (int k = 0; k < 4; ++k) d[c * 4 + k] = __builtin_fmaf(-sum_a, p[c * 4 + k], v[k]);
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      lds_order();
     }
     if (losses) {
       const uint32_t g = on ? (uint32_t)t / n : 0;
@@ -338,10 +367,22 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
       const float c0 = (float)K * (float)live / (float)E;  // sum p = 1: any constant may be taken off; the mean loses least
       float A[NV], s = 0.0f;
       const int32_t *ct = a.counts + (int64_t)g * E;
+      int c[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = id_of<L>(lane, i);
-        A[i] = e < E ? f * ((float)ct[e] - c0) : 0.0f;
+      for (int q = 0; q < NV / 4; ++q) {
+        const int e = id_of<L>(lane, q * 4);
+        typedef int i32x4 __attribute__((ext_vector_type(4), aligned(4)));
+        i32x4 v = {0, 0, 0, 0};
+        if (e + 3 < E) v = *(const i32x4 *)(ct + e);
+        else
+#pragma unroll
+          for (int k = 0; k < 3; ++k) v[k] = e + k < E ? ct[e + k] : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[q * 4 + k] = v[k];
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {  // behind the last id p is 0
+        A[i] = f * ((float)c[i] - c0);
         s = __builtin_fmaf(A[i], p[i], s);
       }
       s = sum_of<L>(s);
@@ -380,7 +421,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
 
 hipError_t launch_route_grad(const RouteGradArgs &a, int score, bool fp32, hipStream_t st) {
   if (a.T == 0) return hipSuccess;
-  with_token(a.E, [&](auto tok) {
+  with_token(a.T, a.E, [&](auto tok) {
     constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES, TOKENS = 4 * (64 / L);
     const int wg = (a.T + TOKENS - 1) / TOKENS;
     with_types(score, fp32, [&](auto sc, auto f32) {

@@ -19,105 +19,98 @@ __device__ __forceinline__ double untagged(double key) {
 }
 
 // the two best of (a, b) and (c, d), each pair in order
-__device__ __forceinline__ void best_two(double &a, double &b, double c, double d) {
-  const double low = fmin(a, c);
-  a = fmax(a, c);
-  b = fmax(low, fmax(b, d));
+template <class V>
+__device__ __forceinline__ void best_two(V &a, V &b, V c, V d) {
+  const V low = a > c ? c : a;
+  a = a > c ? a : c;
+  const V next = b > d ? b : d;
+  b = low > next ? low : next;
 }
 
-template <int L, int NV, int SCORE, bool F32, bool WIDE>
-__device__ __forceinline__ void route_token(const RouteArgs &a, double *groups) {
-  constexpr int PER = 64 / L;
-  const int lane = threadIdx.x & (L - 1), sub = (threadIdx.x & 63) / L;  // of the token; the token of the wave
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = ((int64_t)blockIdx.x * 4 + wave) * PER + sub;
-  const int E = a.E, K = a.K;
-  const bool on = t < a.T && (!a.mask || a.mask[t]);
-  const double none = (double)MOE_NEG_INF;
-  float l[NV];
-  load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
-  float m = 0.0f;  // the largest logit
-  if (WIDE || (SCORE == MOE_SCORE_SOFTMAX && !a.renorm)) m = row_max<L, NV>(l);
-
-  double key[NV];
-  if constexpr (WIDE) {
-    double sum = 0.0;
+// For each of a token's groups put(its best value, its second best, the group), on one lane; value(i): of the lane's i-th id,
+// none where it is not available.  Without a.two the second is not looked for.
+template <int L, int NV, class V, class Value, class Put>
+__device__ __forceinline__ void group_best(const RouteArgs &a, int lane, V none, Value value, Put put) {
+  if (a.span) {  // a group is `span` neighbouring lanes' four values: all groups of a round at once
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (SCORE == MOE_SCORE_SOFTMAX) {
-        key[i] = l[i] > MOE_NEG_INF ? exp((double)l[i] - (double)m) : 0.0;
-        sum += key[i];
-      } else {
-        key[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-      }
-    }
-    if (SCORE == MOE_SCORE_SOFTMAX) {
-      sum = sum_of<L>(sum);
+    for (int c = 0; c < NV / 4; ++c) {
+      V one = none, two = none;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] /= sum;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = id_of<L>(lane, i);
-      bool ok = l[i] > MOE_NEG_INF;
-      if (a.bias && e < E) {
-        const float b = a.bias[e];
-        ok = ok && b > MOE_NEG_INF;
-        key[i] = fmin(key[i] + (double)b, DBL_MAX);
-      }
-      key[i] = ok ? tagged(key[i], e) : none;
+      for (int k = 0; k < 4; ++k) best_two(one, two, value(c * 4 + k), none);
+      auto step = [&](auto ctrl) {
+        constexpr int CTRL = decltype(ctrl)::value;
+        const V other = dpp<CTRL>(one);
+        if (a.two) best_two(one, two, other, dpp<CTRL>(two));
+        else one = one > other ? one : other;
+      };
+      if (a.span > 1) step(std::integral_constant<int, 0xb1>{});
+      if (a.span > 2) step(std::integral_constant<int, 0x4e>{});
+      if (a.span > 4) step(std::integral_constant<int, 0x141>{});
+      if (a.span > 8) step(std::integral_constant<int, 0x140>{});
+      const int at = c * L + lane, g = at >> a.span_log;
+      if ((at & (a.span - 1)) == 0 && g < a.G) put(one, two, g);
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      key[i] = l[i] > MOE_NEG_INF ? tagged((double)(l[i] + 0.0f), id_of<L>(lane, i)) : none;  // one zero
-  }
-
-  if (a.keep < a.G) {
-    const int per = E / a.G;
-    double *gs = groups + (wave * PER + sub) * 64;
+    const int per = a.E / a.G;
     for (int g = 0; g < a.G; ++g) {
-      double one = none, two = none;
+      V one = none, two = none;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const double k = (uint32_t)(id_of<L>(lane, i) - g * per) < (uint32_t)per ? key[i] : none;
-        best_two(one, two, k, none);
-      }
-      if (a.two) {
-        const double first = max_of<L>(one);
-        const double second = max_of<L>(one == first ? two : one);
-        one = first;
-        if (second > none) one = tagged(fmin(untagged(first) + untagged(second), DBL_MAX), g);
-      } else {
-        one = max_of<L>(one);
-      }
-      if (lane == g % L) gs[g] = one;
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    uint64_t kept = 0;
-    for (int g0 = 0; g0 < a.G; g0 += L) {
-      const int g = g0 + lane;
-      const double mine = g < a.G ? gs[g] : none;
-      int better = 0;
-      for (int o = 0; o < a.G; ++o) better += gs[o] > mine;
-      const uint64_t hit = ballot(mine > none && better < a.keep);
-      kept |= (L == 64 ? hit : (hit >> (sub * L)) & ((1ull << (L & 63)) - 1)) << g0;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = id_of<L>(lane, i);
-      if (!(kept >> (fast_div(e, a.div_per) & 63) & 1)) key[i] = none;
+      for (int i = 0; i < NV; ++i)
+        best_two(one, two, (uint32_t)(id_of<L>(lane, i) - g * per) < (uint32_t)per ? value(i) : none, none);
+      const V first = max_of<L>(one);
+      // of the lanes that have the best one, one gives it up
+      const int has = __builtin_ctzll(ballot(one == first) >> (threadIdx.x & 63 & ~(L - 1)));
+      const V second = a.two ? max_of<L>(lane == has ? two : one) : none;
+      if (lane == g % L) put(first, second, g);
     }
   }
+}
 
-  // The lane's three best, in order; a round takes the best of all lanes.  A lane that gave all three looks for the next
-  // ones below the last (of 16 lanes a few in a hundred do, for 8 of 256).
-  double b0, b1, b2;
+// bits of a token's lanes in a ballot
+template <int L>
+__device__ __forceinline__ uint64_t token_bits(uint64_t m) {
+  return L == 64 ? m : (m >> (threadIdx.x & 63 & ~(L - 1))) & ((1ull << (L & 63)) - 1);
+}
+
+// LDS of a token: up to 4 L candidates (before them the groups' scores), its K results
+template <int L>
+struct RouteLds {
+  static constexpr int CANDIDATES = 4 * L;
+  __align__(16) double cand[CANDIDATES + 4];
+  double best[16];
+};
+
+// The groups that a token's ids may come from (bit g), by scores in 64 bits: value(i) as in group_best, tagged.
+template <int L, int NV, class Value>
+__device__ __forceinline__ uint64_t groups_wide(const RouteArgs &a, int lane, double *gs, Value value) {
+  const double none = (double)MOE_NEG_INF;
+  group_best<L, NV>(a, lane, none, value, [&](double one, double two, int g) {
+    if (a.two && two > none) one = untagged(one) + untagged(two);
+    gs[g] = a.two && one > none ? tagged(fmin(one, DBL_MAX), g) : one;
+  });
+  lds_order();
+  uint64_t kept = 0;
+  for (int g0 = 0; g0 < a.G; g0 += L) {
+    const double mine = g0 + lane < a.G ? gs[g0 + lane] : none;
+    int better = 0;
+    for (int o = 0; o < a.G; ++o) better += gs[o] > mine;
+    kept |= token_bits<L>(ballot(mine > none && better < a.keep)) << g0;
+  }
+  lds_order();
+  return kept;
+}
+
+// The best K by rounds, each the best of the lanes' best, in 64 bits: on lane j the key of slot j, or none.  A lane holds its
+// three best in order; one that gave all three looks for the next ones below the last.
+template <int L, int NV, class Key>
+__device__ __forceinline__ double choose_by_rounds(int K, int lane, Key key) {
+  const double none = (double)MOE_NEG_INF;
+  double b0, b1, b2, mine = none;
   auto look = [&](double below) {
     b0 = b1 = b2 = none;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      double k = key[i] < below ? key[i] : none;
+      const double any = key(i), k = any < below ? any : none;
       const double k1 = fmin(b0, k);
       b0 = fmax(b0, k);
       const double k2 = fmin(b1, k1);
@@ -126,7 +119,6 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, double *groups) 
     }
   };
   look((double)__builtin_inf());
-  double mine = none;  // of slot `lane`
   int taken = 0;
   for (int j = 0; j < K; ++j) {
     const double top = max_of<L>(b0);
@@ -142,30 +134,204 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, double *groups) 
       const bool empty = hit && taken == 3;
       const double o0 = b0, o1 = b1, o2 = b2;
       look(top);
-      if (empty) {
-        taken = 0;
-      } else {
-        b0 = o0;
-        b1 = o1;
-        b2 = o2;
-      }
+      b0 = empty ? b0 : o0;
+      b1 = empty ? b1 : o1;
+      b2 = empty ? b2 : o2;
+      taken = empty ? 0 : taken;
     }
   }
+  return mine;
+}
+
+// L lanes a token, NV logits a lane.
+template <int L, int NV, int SCORE, bool F32, bool BIAS>
+__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
+  constexpr int PER = 64 / L;
+  __shared__ RouteLds<L> lds[4 * PER];
+  const int lane = threadIdx.x & (L - 1);
+  RouteLds<L> &my = lds[threadIdx.x / L];
+  const int64_t t = (int64_t)blockIdx.x * (4 * PER) + threadIdx.x / L;
+  const int E = a.E, K = a.K;
+  const bool on = t < a.T && (!a.mask || a.mask[t]), grouped = a.keep < a.G;
+  const double none = (double)MOE_NEG_INF;
+  const float nonef = MOE_NEG_INF;
+  float l[NV];
+  load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
+
+  // What the formulas of softmax need of the whole row: its largest logit, the sum of exponentials.
+  float m = 0.0f, sum = 1.0f;
+  double whole = 1.0;
+  if (SCORE == MOE_SCORE_SOFTMAX ? BIAS || (grouped && a.two) || !a.renorm : BIAS || (grouped && a.two)) m = row_max<L, NV>(l);
+  if (SCORE == MOE_SCORE_SOFTMAX && !a.renorm) {
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum += l[i] > nonef ? exp_neg(l[i] - m) : 0.0f;
+    sum = sum_of<L>(sum);
+  }
+  if (SCORE == MOE_SCORE_SOFTMAX && BIAS) {
+    whole = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) whole += l[i] > nonef ? exp((double)l[i] - (double)m) : 0.0;
+    whole = 1.0 / sum_of<L>(whole);
+  }
+
+  // Scores and keys (a logit; with a bias a score and it) in 64 bits.
+  auto score = [&](float v) -> double {
+    return SCORE == MOE_SCORE_SOFTMAX ? exp((double)v - (double)m) * whole : 1.0 / (1.0 + exp(-(double)v));
+  };
+  auto key_of = [&](float v, int id) -> double {
+    if (!(v > nonef)) return none;
+    if (!BIAS) return tagged((double)(v + 0.0f), id);  // one zero
+    const float b = a.bias[id];
+    return b > nonef ? tagged(fmin(score(v) + (double)b, DBL_MAX), id) : none;
+  };
+
+  // Keys in 32 bits: logits as they are; scores, at most 1, are good to 2^-22, and with a bias the sum to 2^-24 of itself.
+  auto err = [](float v) { return __builtin_fmaf(fabsf(v), 0x1p-23f, 0x1p-21f); };
+  float k[NV];
+  if constexpr (BIAS) {
+    float rest[NV];
+    scores<NV, SCORE>(l, m, k, rest);
+    const bool low = SCORE == MOE_SCORE_SIGMOID && m < -60.0f;  // scores<> took a factor out
+    const float f = SCORE == MOE_SCORE_SOFTMAX ? (float)whole : low ? 0.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int id = id_of<L>(lane, i);
+      const float b = id < E ? a.bias[id] : nonef;
+      k[i] = l[i] > nonef && b > nonef ? fminf(__builtin_fmaf(k[i], f, b), FLT_MAX) : nonef;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) k[i] = l[i];
+  }
+  if (grouped) {
+    float *gs = (float *)my.cand;  // what a group's score is at least; 64 on, at most
+    const bool exact = !BIAS && !a.two;
+    auto bounds = [&](float one, float two, int g) {
+      const bool both = a.two && two > nonef;
+      const float s = both ? fminf(one + two, FLT_MAX) : one;
+      const float e = exact ? 0.0f : both ? err(one) + err(two) + fabsf(s) * 0x1p-23f : err(one);
+      gs[g] = one > nonef ? s - e : nonef;
+      gs[64 + g] = one > nonef ? s + e : nonef;
+    };
+    if (!BIAS && a.two) {
+      float s[NV], rest[NV];
+      scores<NV, SCORE>(l, m, s, rest);
+      const bool low = SCORE == MOE_SCORE_SIGMOID && m < -60.0f;
+      group_best<L, NV>(a, lane, nonef, [&](int i) { return l[i] > nonef ? (low ? 0.0f : s[i]) : nonef; }, bounds);
+    } else {
+      group_best<L, NV>(a, lane, nonef, [&](int i) { return k[i]; }, bounds);
+    }
+    lds_order();
+    uint64_t kept = 0;
+    bool open = false;
+    for (int g0 = 0; g0 < a.G; g0 += L) {
+      const int g = g0 + lane;
+      const float least = g < a.G ? gs[g] : nonef, most = g < a.G ? gs[64 + g] : nonef;
+      const bool some = most > nonef;
+      int above = 0, near = -1;
+      bool in;
+      if (exact) {
+#pragma unroll 4
+        for (int o = 0; o < a.G; ++o) above += gs[o] > most || (gs[o] == most && o < g);
+        in = some && above < a.keep;
+      } else {
+#pragma unroll 4
+        for (int o = 0; o < a.G; ++o) {
+          above += gs[o] > most;
+          near += gs[64 + o] >= least;
+        }
+        in = some && near < a.keep;
+        open = open || (some && !in && above < a.keep);
+      }
+      kept |= token_bits<L>(ballot(in)) << g0;
+    }
+    lds_order();
+    if (ballot(open))  // two groups too near one another at the border: some of 10^5 tokens
+      kept = groups_wide<L, NV>(a, lane, my.cand, [&](int i) {
+        const int id = id_of<L>(lane, i);
+        return BIAS ? key_of(l[i], id) : l[i] > nonef ? tagged(score(l[i]), id) : none;
+      });
+    if (a.span) {
+#pragma unroll
+      for (int c = 0; c < NV / 4; ++c) {
+        const bool in = kept >> ((c * L + lane) >> a.span_log & 63) & 1;
+#pragma unroll
+        for (int i = c * 4; i < c * 4 + 4; ++i) {
+          l[i] = in ? l[i] : nonef;
+          k[i] = in ? k[i] : nonef;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (!(kept >> (fast_div(id_of<L>(lane, i), a.div_per) & 63) & 1)) l[i] = k[i] = nonef;
+    }
+  }
+
+  // The K-th largest of the lanes' largest is a bound that at least K keys reach; the few that reach it are compared with one
+  // another, each by a lane of its own.
+  float top = nonef;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) top = fmaxf(top, k[i]);
+  if (BIAS) top -= err(top);
+  float *tops = (float *)my.cand;
+  tops[lane] = top;
+  if (lane < 16) my.best[lane] = none;
+  lds_order();
+  int rank = 0;
+#pragma unroll
+  for (int o = 0; o < L; o += 4) {
+    const f32x4 v = *(const f32x4 *)(tops + o);
+    rank += (v[0] > top) + (v[1] > top) + (v[2] > top) + (v[3] > top);
+  }
+  lds_order();
+  float bound = fold<L>(rank < K ? top : __builtin_inff(), [](float x, float y) { return fminf(x, y); });
+  if (BIAS) bound -= 2.0f * err(bound);  // of a key that reaches it, and of the subtraction
+  bound = fmaxf(bound, -FLT_MAX);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) n += k[i] >= bound;
+  const int upto = wave_inclusive_sum(n);  // over the wave
+  const int first = threadIdx.x & 63 & ~(L - 1), last = __shfl(upto, (first - 1) & 63);
+  const int before = first ? last : 0;  // in the wave's other tokens
+  int at = upto - n - before;
+  n = __shfl(upto, L - 1, L) - before;
+  double mine = none;
+  if (ballot(n > RouteLds<L>::CANDIDATES)) {  // rows of one value, or nearly
+    mine = choose_by_rounds<L, NV>(K, lane, [&](int i) { return key_of(l[i], id_of<L>(lane, i)); });
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (k[i] >= bound) my.cand[at++] = __hiloint2double(__float_as_int(l[i]), id_of<L>(lane, i));
+    lds_order();
+    for (int c = lane; ballot(c < n); c += L)
+      if (c < n) my.cand[c] = key_of(__int_as_float(__double2hiint(my.cand[c])), __double2loint(my.cand[c]));
+    if (lane < 4) my.cand[n + lane] = none;
+    lds_order();
+    for (int c = lane; ballot(c < n); c += L) {
+      const double key = c < n ? my.cand[c] : none;
+      int r = 0;
+      for (int o = 0; o < n; o += 4)
+        r += (my.cand[o] > key) + (my.cand[o + 1] > key) + (my.cand[o + 2] > key) + (my.cand[o + 3] > key);
+      if (key > none && r < K) my.best[r] = key;
+    }
+    lds_order();
+    if (lane < K) mine = my.best[lane];
+  }
+
   const bool some = mine > none;
   const int id = some ? id_in(mine) : -1;
-  float lj = WIDE ? (some ? logit_at(a.logits, F32, t * E + id) : 0.0f) : some ? (float)mine : 0.0f;  // the tag is far below its last bit
+  // without a bias the key is the logit, its tag far below the last bit of 32
+  const float lj = !some ? 0.0f : BIAS ? logit_at(a.logits, F32, t * E + id) : (float)mine;
   float w;
   if (a.renorm) {
-    const float q = !some ? MOE_NEG_INF : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
+    const float q = !some ? nonef : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
     const float mq = max_of<L>(q);
     w = some ? exp_neg(q - mq) : 0.0f;
-    const float sum = sum_of<L>(w);
-    w = some ? w / sum * a.scale : 0.0f;
+    const float all = sum_of<L>(w);
+    w = some ? w / all * a.scale : 0.0f;
   } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sum += l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
-    sum = sum_of<L>(sum);
     w = some ? exp_neg(lj - m) / sum * a.scale : 0.0f;
   } else {
     w = some ? 1.0f / (1.0f + expf(-lj)) * a.scale : 0.0f;
@@ -176,24 +342,18 @@ __device__ __forceinline__ void route_token(const RouteArgs &a, double *groups) 
   }
 }
 
-template <int L, int NV, int SCORE, bool F32, bool WIDE>
-__global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
-  __shared__ double groups[4 * (64 / L) * 64];
-  route_token<L, NV, SCORE, F32, WIDE>(a, groups);
-}
-
 template <int L, int NV>
-static void launch_sized(const RouteArgs &a, int score, bool fp32, bool wide, hipStream_t st) {
+static void launch_sized(const RouteArgs &a, int score, bool fp32, hipStream_t st) {
   constexpr int TOKENS = 4 * (64 / L);  // a workgroup
   const dim3 grid((unsigned)((a.T + TOKENS - 1) / TOKENS)), block(256);
-  auto go = [&](auto sc, auto f32, auto wd) {
-    hipLaunchKernelGGL((route_kernel<L, NV, decltype(sc)::value, decltype(f32)::value, decltype(wd)::value>), grid, block, 0,
+  auto go = [&](auto sc, auto f32, auto bias) {
+    hipLaunchKernelGGL((route_kernel<L, NV, decltype(sc)::value, decltype(f32)::value, decltype(bias)::value>), grid, block, 0,
                        st, a);
   };
   auto types = [&](auto sc) {
-    if (fp32 && wide) go(sc, std::true_type{}, std::true_type{});
+    if (fp32 && a.bias) go(sc, std::true_type{}, std::true_type{});
     else if (fp32) go(sc, std::true_type{}, std::false_type{});
-    else if (wide) go(sc, std::false_type{}, std::true_type{});
+    else if (a.bias) go(sc, std::false_type{}, std::true_type{});
     else go(sc, std::false_type{}, std::false_type{});
   };
   if (score == MOE_SCORE_SOFTMAX) types(std::integral_constant<int, MOE_SCORE_SOFTMAX>{});
@@ -203,9 +363,11 @@ static void launch_sized(const RouteArgs &a, int score, bool fp32, bool wide, hi
 hipError_t launch_route(const RouteArgs &a_, int score, bool fp32, hipStream_t st) {
   RouteArgs a = a_;
   if (a.T == 0) return hipSuccess;
-  a.div_per = div_magic(a.E / a.G);
-  const bool wide = a.bias || (a.two && a.keep < a.G);
-  with_token(a.E, [&](auto tok) { launch_sized<decltype(tok)::LANES, decltype(tok)::VALUES>(a, score, fp32, wide, st); });
+  const int per = a.E / a.G, quads = per / 4;
+  a.div_per = div_magic(per);
+  a.span = per % 4 == 0 && (quads & (quads - 1)) == 0 && quads <= 16 ? quads : 0;
+  a.span_log = a.span ? __builtin_ctz(a.span) : 0;
+  with_token(a.T, a.E, [&](auto tok) { launch_sized<decltype(tok)::LANES, decltype(tok)::VALUES>(a, score, fp32, st); });
   return hipGetLastError();
 }
 

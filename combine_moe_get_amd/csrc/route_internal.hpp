@@ -17,7 +17,10 @@ struct RouteArgs {
   int32_t T, E, K, G, keep;
   int32_t two, renorm;
   float scale;
-  uint32_t div_per;      // div_magic of the ids of a group; set by the launcher
+  // set by the launcher: div_magic of the ids of a group; lanes that hold four each of them, if these are a power of two up
+  // to 16 (else 0), and its logarithm
+  uint32_t div_per;
+  int32_t span, span_log;
 };
 hipError_t launch_route(const RouteArgs &a, int score, bool fp32, hipStream_t stream);
 
@@ -56,20 +59,23 @@ hipError_t launch_route_grad(const RouteGradArgs &a, int score, bool fp32, hipSt
 // ---- a token on L lanes of a wave (16, 32 or 64), 64 / L tokens a wave --------------------------------
 //
 // A lane holds NV of its token's logits, four neighbouring ids at a time: value i is of id (i / 4 * L + lane) * 4 + i % 4.
-// Sixteen lanes are a DPP row, whose folds need no LDS; and what a wave does once it does for four tokens: the K best of
-// 256 ids of 16384 tokens took 9 us on 64 lanes a token, XX on 16.
+// Sixteen lanes are a DPP row, whose folds need no LDS; what a wave does once it does for all its tokens, but few tokens
+// leave the chip empty, and many values a lane take its registers.
 template <int L, int NV>
 struct Token {
   static constexpr int LANES = L, VALUES = NV;
 };
 
-// f(Token) for the least that holds E ids
+// f(Token) for T tokens of E ids.  Measured in us by lanes a token, graph replays (a launch is 2.9 of them): the choice of 8 of
+// 256 at 4096 tokens 5.0 on 16, 4.2 on 32, 4.9 on 64, at 65536 25.8, 22.2, 35.3; of 128 at 4096 tokens 4.3 on 16, 3.8 on 32,
+// at 16384 5.0, 5.9; of 512 at 4096 4.8 on 32, 5.3 on 64, at 65536 46.7, 44.7, its gradient at 4096 11.2, 10.2.
 template <class F>
-inline void with_token(int E, F &&f) {
+inline void with_token(int T, int E, F &&f) {
   if (E <= 64) f(Token<16, 4>{});
+  else if (E <= 128 && T < 8192) f(Token<32, 4>{});
   else if (E <= 128) f(Token<16, 8>{});
-  else if (E <= 256) f(Token<16, 16>{});
-  else if (E <= 512) f(Token<32, 16>{});
+  else if (E <= 256) f(Token<32, 8>{});
+  else if (E <= 512) f(Token<64, 8>{});
   else if (E <= 1024) f(Token<64, 16>{});
   else f(Token<64, 32>{});
 }
@@ -111,6 +117,9 @@ template <int L, class V>
 __device__ __forceinline__ V sum_of(V v) {
   return fold<L>(v, [](V a, V b) { return a + b; });
 }
+
+// LDS accesses of a wave are in order; this keeps the compiler to it
+__device__ __forceinline__ void lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // a logit that counts: +inf as the largest finite value, NaN as -inf
 __device__ __forceinline__ float usable(float l) { return l > MOE_NEG_INF ? fminf(l, FLT_MAX) : MOE_NEG_INF; }

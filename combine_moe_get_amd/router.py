@@ -10,7 +10,7 @@ from collections import namedtuple
 import torch
 
 from . import binding as B
-from .experts import ExpertsCall, _device_of, _ptr
+from .experts import ExpertsCall, _device_of, _ptr, _result
 
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GROUP_MAX, GROUP_TOP2 = 0, 1
@@ -103,18 +103,14 @@ def prepare_route(shape, logits, bias=None, x_active_mask=None, topk_idx=None, t
     """Checked, marshalled moe_route call; see route()."""
     dev, fp32 = _logits(shape, logits, "route")
     T, E, K = shape.num_tokens, shape.num_ids, shape.topk
-    if topk_idx is None:
-        topk_idx = torch.empty((T, K), dtype=torch.int32, device=dev)
-    if topk_weights is None:
-        topk_weights = torch.empty((T, K), dtype=torch.float32, device=dev)
+    topk_idx, idx_p = _result(topk_idx, "topk_idx", torch.int32, (T, K), dev)
+    topk_weights, w_p = _result(topk_weights, "topk_weights", torch.float32, (T, K), dev)
     args = [
         ctypes.byref(shape), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
         _ptr(bias, "bias", B.F32, E, dev, required=False),
         _ptr(x_active_mask, "x_active_mask", B.U8, T, dev, required=False),
-        _ptr(topk_idx, "topk_idx", B.I32, T * K, dev),
-        _ptr(topk_weights, "topk_weights", B.F32, T * K, dev),
-        None,
+        idx_p, w_p, None,
     ]
     return ExpertsCall(_lib().moe_route, args, "route", (shape, logits, bias, x_active_mask),
                        Route(topk_idx, topk_weights), dev)
@@ -138,21 +134,21 @@ def prepare_balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, w
     need = balance_workspace_size(shape, balance)
     if need == 0:
         raise B.MoeGetError("balance_loss", -4 if 4096 < S and T % S == 0 else -2)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
-    r = BalanceLoss(torch.empty(2, **f32), torch.empty((S, E), **i32), torch.empty((S, E), **f32), torch.empty(S, **i32))
+    workspace, ws_p = _result(workspace, "workspace", torch.uint8, (need,), dev)
+    losses, losses_p = _result(None, "losses", torch.float32, (2,), dev)
+    counts, counts_p = _result(None, "counts", torch.int32, (S, E), dev)
+    sums, sums_p = _result(None, "prob_sums", torch.float32, (S, E), dev)
+    tokens, tokens_p = _result(None, "segment_tokens", torch.int32, (S,), dev)
     args = [
         ctypes.byref(shape), ctypes.byref(balance), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
         _ptr(topk_idx, "topk_idx", B.I32, T * K, dev),
         _ptr(x_active_mask, "x_active_mask", B.U8, T, dev, required=False),
-        *(t.data_ptr() for t in r),
-        _ptr(workspace, "workspace", (torch.uint8,), need, dev), workspace.numel(),
-        None,
+        losses_p, counts_p, sums_p, tokens_p, ws_p, workspace.numel(), None,
     ]
     return ExpertsCall(_lib().moe_balance_loss, args, "balance_loss",
-                       (shape, balance, logits, topk_idx, x_active_mask, workspace), r, dev)
+                       (shape, balance, logits, topk_idx, x_active_mask, workspace),
+                       BalanceLoss(losses, counts, sums, tokens), dev)
 
 
 def balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, workspace=None, stream=None):
@@ -181,8 +177,7 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
     S = 0
     if balance is not None:
         S, counts, tokens = balance.segments, balance_loss.counts, balance_loss.segment_tokens
-    if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    out, out_p = _result(out, "out", logits.dtype, (T, E), dev)
     args = [
         ctypes.byref(shape), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
@@ -194,8 +189,7 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
         _ptr(counts, "counts", B.I32, S * E, dev, required=False),
         _ptr(tokens, "segment_tokens", B.I32, S, dev, required=False),
         _ptr(grad_losses, "grad_losses", B.F32, 2, dev, required=False),
-        _ptr(out, "out", (logits.dtype,), T * E, dev),
-        None,
+        out_p, None,
     ]
     return ExpertsCall(_lib().moe_route_grad, args, "route_grad",
                        (shape, logits, topk_idx, grad_topk_weights, dst_row, x_active_mask, balance, counts, tokens, grad_losses),
