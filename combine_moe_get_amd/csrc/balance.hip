@@ -5,9 +5,24 @@ namespace moe {
 
 // ---- the losses ----------------------------------------------------------------------------------
 
-// Workgroups that share a segment's tokens.
-static int slices(int T, int S) {
-  const int n = T / S, most = (n + 31) / 32, want = (1024 + S - 1) / S;
+constexpr int kSumGroups = 1024;
+
+// As with_token: here all four tokens of a wave pay at any number (4096 of 256 ids: 12.2 us on 16 lanes, 13.6 on 32).
+template <class F>
+static void with_sums_token(int E, F &&f) {
+  if (E <= 64) f(Token<16, 4>{});
+  else if (E <= 128) f(Token<16, 8>{});
+  else if (E <= 256) f(Token<16, 16>{});
+  else if (E <= 512) f(Token<32, 16>{});
+  else if (E <= 1024) f(Token<64, 16>{});
+  else f(Token<64, 32>{});
+}
+
+// Workgroups that share a segment's tokens: twice as many tokens each as it takes at a time, up to some four a CU in all.
+static int slices(int T, int E, int S) {
+  int tokens = 0;
+  with_sums_token(E, [&](auto tok) { tokens = 4 * (64 / decltype(tok)::LANES); });
+  const int n = T / S, most = (n + 2 * tokens - 1) / (2 * tokens), want = (kSumGroups + S - 1) / S;
   const int L = most < want ? most : want;
   return L < 1 ? 1 : L;
 }
@@ -40,21 +55,16 @@ static __host__ __device__ BalanceSpace balance_space(char *ws, int L, int E, in
   return b;
 }
 
-size_t balance_workspace(int T, int E, int S) { return balance_space(nullptr, slices(T, S), E, S).bytes; }
+size_t balance_workspace(int T, int E, int S) { return balance_space(nullptr, slices(T, E, S), E, S).bytes; }
 
-// As with_token: here all four tokens of a wave pay at any number (4096 of 256 ids: 12.2 us on 16 lanes, 13.6 on 32).
-template <class F>
-static void with_sums_token(int E, F &&f) {
-  if (E <= 64) f(Token<16, 4>{});
-  else if (E <= 128) f(Token<16, 8>{});
-  else if (E <= 256) f(Token<16, 16>{});
-  else if (E <= 512) f(Token<32, 16>{});
-  else if (E <= 1024) f(Token<64, 16>{});
-  else f(Token<64, 32>{});
+// balance_coef E / (segments K T_g^2)
+__device__ __forceinline__ double segment_factor(const BalanceArgs &a, int live) {
+  return live > 0 ? (double)a.balance_coef * a.E / ((double)a.S * a.K * live * live) : 0.0;
 }
 
-// First kernel: a workgroup sums over a slice of a segment's tokens.
-template <int L, int NV, int SCORE, bool F32>
+// First kernel: a workgroup sums over a slice of a segment's tokens; ALONE: the only workgroup over all tokens of each segment
+// in turn, and writes the results itself.
+template <int L, int NV, int SCORE, bool F32, bool ALONE>
 __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int slices) {
   constexpr int TOKENS = 4 * (64 / L);  // at a time
   __shared__ __align__(16) float red[TOKENS][L * NV];
@@ -62,71 +72,113 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
   __shared__ double zs[TOKENS];
   __shared__ int lives[TOKENS];
   const int lane = threadIdx.x & (L - 1), sub = threadIdx.x / L;
-  const int E = a.E, K = a.K, n = a.T / a.S, g = blockIdx.x / slices, s = blockIdx.x - g * slices;
-  const BalanceSpace ws = balance_space(a.ws, slices, E, a.S);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *ws.counter = 0;
-  for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
-  __syncthreads();
-  const int64_t t0 = (int64_t)g * n + (int64_t)n * s / slices, t1 = (int64_t)g * n + (int64_t)n * (s + 1) / slices;
-  float acc[NV];
+  const int E = a.E, K = a.K, n = a.T / a.S, s = ALONE ? 0 : blockIdx.x % slices;
+  double loss = 0.0, all_z = 0.0;  // ALONE: of this thread's columns; of all tokens
+  int all_live = 0;
+  for (int g = ALONE ? 0 : blockIdx.x / slices; g < (ALONE ? a.S : blockIdx.x / slices + 1); ++g) {
+    for (int e = threadIdx.x; e < E; e += 256) cnt[e] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)g * n + (int64_t)n * s / slices, t1 = (int64_t)g * n + (int64_t)n * (s + 1) / slices;
+    float acc[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
-  double z = 0.0;
-  int live = 0;
-  for (int64_t tb = t0; tb < t1; tb += TOKENS) {  // the same for all lanes of the wave
-    const int64_t t = tb + sub;
-    const bool on = t < t1 && (!a.mask || a.mask[t]);
-    float l[NV], p[NV], rest[NV];
-    load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
-    int id = on && lane < K ? a.idx[t * K + lane] : -1;
-    const float m = row_max<L, NV>(l);
-    const bool counts = m > MOE_NEG_INF;
-    scores<NV, SCORE>(l, m, p, rest);
-    float sum = 0.0f;
+    for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
+    double z = 0.0;
+    int live = 0;
+    float next[NV];
+    int next_id = -1;
+    auto fetch = [&](int64_t tb) {
+      const int64_t t = tb + sub;
+      const bool on = t < t1 && (!a.mask || a.mask[t]);
+      load_logits<L, NV, F32>(a.logits, t, E, lane, on, next);
+      next_id = on && lane < K ? a.idx[t * K + lane] : -1;
+    };
+    fetch(t0);
+    for (int64_t tb = t0; tb < t1; tb += TOKENS) {  // the same for all lanes of the wave
+      float l[NV], p[NV], rest[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sum += p[i];
-    sum = sum_of<L>(sum);
-    const float r = counts ? 1.0f / sum : 0.0f;
+      for (int i = 0; i < NV; ++i) l[i] = next[i];
+      const int id = next_id;
+      if (tb + TOKENS < t1) fetch(tb + TOKENS);  // under way meanwhile
+      const float m = row_max<L, NV>(l);
+      const bool counts = m > MOE_NEG_INF;
+      scores<NV, SCORE>(l, m, p, rest);
+      float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(p[i], r, acc[i]);
-    if (a.z_coef != 0.0f) {
-      if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-        sum = 0.0f;
+      for (int i = 0; i < NV; ++i) sum += p[i];
+      sum = sum_of<L>(sum);
+      const float r = counts ? 1.0f / sum : 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sum += l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
-        sum = sum_of<L>(sum);
+      for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(p[i], r, acc[i]);
+      if (a.z_coef != 0.0f) {
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+          sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) sum += l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+          sum = sum_of<L>(sum);
+        }
+        const double lse = counts ? m + logf(sum) : 0.0f;
+        z += lse * lse;
       }
-      const double lse = counts ? (double)m + log((double)sum) : 0.0;
-      z += lse * lse;
+      live += counts;
+      if (counts && id >= 0 && id < E) atomicAdd(&cnt[id], 1);  // integers: in any order
     }
-    live += counts;
-    if (counts && id >= 0 && id < E) atomicAdd(&cnt[id], 1);  // integers: in any order
-  }
 #pragma unroll
-  for (int c = 0; c < NV / 4; ++c)
-    *(f32x4 *)&red[sub][id_of<L>(lane, c * 4)] = f32x4{acc[c * 4], acc[c * 4 + 1], acc[c * 4 + 2], acc[c * 4 + 3]};
-  if (lane == 0) {
-    zs[sub] = z;
-    lives[sub] = live;
-  }
-  __syncthreads();
-  const int64_t slot = (int64_t)blockIdx.x;
-  for (int e = threadIdx.x; e < E; e += 256) {
-    float v = red[0][e];
+    for (int c = 0; c < NV / 4; ++c)
+      *(f32x4 *)&red[sub][id_of<L>(lane, c * 4)] = f32x4{acc[c * 4], acc[c * 4 + 1], acc[c * 4 + 2], acc[c * 4 + 3]};
+    if (lane == 0) {
+      zs[sub] = z;
+      lives[sub] = live;
+    }
+    __syncthreads();
+    z = zs[0];
+    live = lives[0];
 #pragma unroll
-    for (int k = 1; k < TOKENS; ++k) v += red[k][e];
-    ws.sum[slot * E + e] = v;
-    ws.cnt[slot * E + e] = cnt[e];
-  }
-  if (threadIdx.x == 0) {
     for (int k = 1; k < TOKENS; ++k) {
       z += zs[k];
       live += lives[k];
     }
-    ws.z[slot] = z;
-    ws.live[slot] = live;
+    const double f = ALONE ? segment_factor(a, live) : 0.0;
+    BalanceSpace ws;
+    if (!ALONE) ws = balance_space(a.ws, slices, E, a.S);
+    for (int e = threadIdx.x; e < E; e += 256) {
+      float v = red[0][e];
+#pragma unroll
+      for (int k = 1; k < TOKENS; ++k) v += red[k][e];
+      if constexpr (ALONE) {
+        a.sums[(int64_t)g * E + e] = v;
+        a.counts[(int64_t)g * E + e] = cnt[e];
+        loss += f * cnt[e] * (double)v;
+      } else {
+        ws.sum[(int64_t)blockIdx.x * E + e] = v;
+        ws.cnt[(int64_t)blockIdx.x * E + e] = cnt[e];
+      }
+    }
+    if constexpr (ALONE) {
+      if (threadIdx.x == 0) a.tokens[g] = live;
+      all_z += z;
+      all_live += live;
+      __syncthreads();
+    } else if (threadIdx.x == 0) {
+      ws.z[blockIdx.x] = z;
+      ws.live[blockIdx.x] = live;
+      if (blockIdx.x == 0) *ws.counter = 0;
+    }
+  }
+  if constexpr (ALONE) {
+    loss = sum_of<64>(loss);
+    if ((threadIdx.x & 63) == 0) zs[threadIdx.x >> 6] = loss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      a.losses[0] = (float)((zs[0] + zs[1]) + (zs[2] + zs[3]));
+      a.losses[1] = all_live > 0 ? (float)((double)a.z_coef * all_z / all_live) : 0.0f;
+    }
   }
 }
+
+// Whether a single workgroup does it all: rounds of its tokens, in values a lane.  Against two launches, us in graph replays
+// (and the second launch costs the host 3 more): 16 tokens of 64 ids 3.2 / 6.9, 128 8.2 / 8.3, 256 13.8 / 8.5; 16 of 256
+// 4.9 / 8.2, 64 10.5 / 10.2.
+constexpr int kAloneValues = 32;
 
 // Second kernel: a workgroup C columns of a segment, 1024 / C parts of its slices; the last one to finish adds the parts of
 // the losses, in order.
@@ -166,8 +218,7 @@ __global__ void __launch_bounds__(1024) balance_losses_kernel(BalanceArgs a, int
       a.sums[(int64_t)g * E + e] = (float)sum;
     }
     if (e == 0) a.tokens[g] = n;
-    const double f = n > 0 ? (double)a.balance_coef * E / ((double)a.S * a.K * n * n) : 0.0;
-    const double mine = sum_of<64>(f * cnt * sum);
+    const double mine = sum_of<64>(segment_factor(a, n) * cnt * sum);
     if ((tid & 63) == 0) reds[tid >> 6] = mine;
   }
   __syncthreads();
@@ -223,16 +274,25 @@ static void with_types(int score, bool fp32, F &&f) {
 }
 
 hipError_t launch_balance(const BalanceArgs &a, int score, bool fp32, hipStream_t st) {
-  const int n = slices(a.T, a.S);
+  const int n = slices(a.T, a.E, a.S);
+  bool alone = false;
   with_sums_token(a.E, [&](auto tok) {
-    constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES;
+    constexpr int L = decltype(tok)::LANES, NV = decltype(tok)::VALUES, TOKENS = 4 * (64 / L);
+    alone = NV <= 16 && (int64_t)a.S * ((a.T / a.S + TOKENS - 1) / TOKENS) * NV <= kAloneValues;
     with_types(score, fp32, [&](auto sc, auto f32) {
-      hipLaunchKernelGGL((balance_sums_kernel<L, NV, decltype(sc)::value, decltype(f32)::value>), dim3((unsigned)(a.S * n)),
-                         dim3(256), 0, st, a, n);
+      constexpr int SC = decltype(sc)::value;
+      constexpr bool F32 = decltype(f32)::value;
+      if constexpr (NV <= 16) {
+        if (alone) {
+          hipLaunchKernelGGL((balance_sums_kernel<L, NV, SC, F32, true>), dim3(1), dim3(256), 0, st, a, 1);
+          return;
+        }
+      }
+      hipLaunchKernelGGL((balance_sums_kernel<L, NV, SC, F32, false>), dim3((unsigned)(a.S * n)), dim3(256), 0, st, a, n);
     });
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || alone) return e;
   if (n >= 16) hipLaunchKernelGGL((balance_losses_kernel<64>), dim3((unsigned)(a.S * ((a.E + 63) / 64))), dim3(1024), 0, st, a, n);
   else hipLaunchKernelGGL((balance_losses_kernel<256>), dim3((unsigned)(a.S * ((a.E + 255) / 256))), dim3(1024), 0, st, a, n);
   return hipGetLastError();

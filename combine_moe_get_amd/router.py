@@ -103,8 +103,8 @@ def prepare_route(shape, logits, bias=None, x_active_mask=None, topk_idx=None, t
     """Checked, marshalled moe_route call; see route()."""
     dev, fp32 = _logits(shape, logits, "route")
     T, E, K = shape.num_tokens, shape.num_ids, shape.topk
-    topk_idx, idx_p = _result(topk_idx, "topk_idx", torch.int32, (T, K), dev)
-    topk_weights, w_p = _result(topk_weights, "topk_weights", torch.float32, (T, K), dev)
+    topk_idx, idx_p = _result(topk_idx, "topk_idx", torch.int32, (T, K), (K, 1), dev)
+    topk_weights, w_p = _result(topk_weights, "topk_weights", torch.float32, (T, K), (K, 1), dev)
     args = [
         ctypes.byref(shape), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
@@ -134,11 +134,11 @@ def prepare_balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, w
     need = balance_workspace_size(shape, balance)
     if need == 0:
         raise B.MoeGetError("balance_loss", -4 if 4096 < S and T % S == 0 else -2)
-    workspace, ws_p = _result(workspace, "workspace", torch.uint8, (need,), dev)
-    losses, losses_p = _result(None, "losses", torch.float32, (2,), dev)
-    counts, counts_p = _result(None, "counts", torch.int32, (S, E), dev)
-    sums, sums_p = _result(None, "prob_sums", torch.float32, (S, E), dev)
-    tokens, tokens_p = _result(None, "segment_tokens", torch.int32, (S,), dev)
+    workspace, ws_p = _result(workspace, "workspace", torch.uint8, (need,), (1,), dev)
+    losses, losses_p = _result(None, "losses", torch.float32, (2,), (1,), dev)
+    counts, counts_p = _result(None, "counts", torch.int32, (S, E), (E, 1), dev)
+    sums, sums_p = _result(None, "prob_sums", torch.float32, (S, E), (E, 1), dev)
+    tokens, tokens_p = _result(None, "segment_tokens", torch.int32, (S,), (1,), dev)
     args = [
         ctypes.byref(shape), ctypes.byref(balance), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
@@ -177,7 +177,7 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
     S = 0
     if balance is not None:
         S, counts, tokens = balance.segments, balance_loss.counts, balance_loss.segment_tokens
-    out, out_p = _result(out, "out", logits.dtype, (T, E), dev)
+    out, out_p = _result(out, "out", logits.dtype, (T, E), (E, 1), dev)
     args = [
         ctypes.byref(shape), fp32,
         _ptr(logits, "logits", (logits.dtype,), T * E, dev),
