@@ -42,126 +42,139 @@ __device__ __forceinline__ float max16(float v) {
 constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is left
 
 // ---- forward: 16 lanes a block of 128 columns of a row, 8 of each half a lane -----------------------
-constexpr int kFwdBlocks = 2;  // blocks of 128 columns that a thread has under way
+//
+// One pass, bound by memory: 32768 rows of 2 x 2048 105 us with codes (541 MB, 5.2 TB/s; a large copy reaches 5.1), 68
+// without (403 MB, 5.9 TB/s).  Stores go past the caches (106 and 85 us where they do not: the lines they would leave there
+// are the next reader's only where rows are few).  Two blocks a thread take 108, four more registers than it pays.
 template <bool KEEP>
 __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
   const int sub = threadIdx.x & 15, I = a.I;
   const uint32_t nb = (uint32_t)(I + 127) / 128;
-  for (uint64_t first = (uint64_t)blockIdx.x * (16 * kFwdBlocks); first < (uint64_t)a.rows * nb;
-       first += (uint64_t)gridDim.x * (16 * kFwdBlocks)) {
-    const uint64_t row0 = first / nb;
-    const uint32_t rem = (uint32_t)(first - row0 * nb);
-    int64_t r[kFwdBlocks];
-    uint32_t b[kFwdBlocks];
-    bool in[kFwdBlocks];
-    u32x4 gv[kFwdBlocks], uv[kFwdBlocks];
-    float w[kFwdBlocks];
-#pragma unroll
-    for (int k = 0; k < kFwdBlocks; ++k) {
-      const uint32_t i = rem + k * 16 + (threadIdx.x >> 4), q = i / nb;
-      r[k] = (int64_t)row0 + q;
-      b[k] = i - q * nb;
-      const int col = (int)b[k] * 128 + sub * 8;
-      in[k] = r[k] < a.rows && row_used(a.g, r[k]) && col < I;
-      gv[k] = uv[k] = u32x4{0u, 0u, 0u, 0u};
-      w[k] = 1.0f;
-      if (in[k]) {
-        const uint16_t *p = a.h0 + r[k] * 2 * I + col;
-        gv[k] = *(const u32x4 *)p;
-        uv[k] = *(const u32x4 *)(p + I);
-        if (a.w) w[k] = a.w[r[k]];
-      }
+  for (uint64_t first = (uint64_t)blockIdx.x * 16; first < (uint64_t)a.rows * nb; first += (uint64_t)gridDim.x * 16) {
+    const uint64_t row0 = first / nb;  // the workgroup's 16 blocks, in the order of rows
+    const uint32_t i = (uint32_t)(first - row0 * nb) + (threadIdx.x >> 4), q = i / nb, b = i - q * nb;
+    const int64_t r = (int64_t)row0 + q;
+    const int col = (int)b * 128 + sub * 8;
+    const bool in = r < a.rows && row_used(a.g, r) && col < I;
+    u32x4 gv = {0u, 0u, 0u, 0u}, uv = gv;
+    float w = 1.0f;
+    if (in) {
+      const uint16_t *p = a.h0 + r * 2 * I + col;
+      gv = *(const u32x4 *)p;
+      uv = *(const u32x4 *)(p + I);
+      if (a.w) w = a.w[r];
     }
+    float g[8], u[8], h[8];
+    unpack8(gv, g);
+    unpack8(uv, u);
 #pragma unroll
-    for (int k = 0; k < kFwdBlocks; ++k) {
-      const int col = (int)b[k] * 128 + sub * 8;
-      float g[8], u[8], h[8];
-      unpack8(gv[k], g);
-      unpack8(uv[k], u);
+    for (int e = 0; e < 8; ++e) {
+      const Logistic s = logistic(g[e]);
+      h[e] = s.s1 * g[e] * u[e] * s.s2 * w;
+    }
+    if (in) __builtin_nontemporal_store(pack8(h), (u32x4 *)(a.out + r * I + col));
+    if constexpr (KEEP) {
+      auto keep = [&](const float *x, int half) {
+        float m = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const Logistic s = logistic(g[e]);
-        h[e] = s.s1 * g[e] * u[e] * s.s2 * w[k];
-      }
-      if (in[k]) *(u32x4 *)(a.out + r[k] * I + col) = pack8(h);
-      if constexpr (KEEP) {
-        auto keep = [&](const float *x, int half) {
-          float m = 0.0f;
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+        m = max16(m);  // by all lanes
+        const float dyn = m > 0.0f ? 127.0f * (1.0f / m) : 0.0f;
+        if (!in) return;
+        int c[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-          m = max16(m);
-          const float dyn = m > 0.0f ? 127.0f * (1.0f / m) : 0.0f;
-          if (!in[k]) return;
-          int c[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) c[e] = sat_code(x[e] * dyn);
-          *(u32x2 *)(a.codes + r[k] * 2 * I + half * I + col) =
-              u32x2{pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7])};
-          if (sub == 0) a.scales[(r[k] * 2 + half) * nb + b[k]] = m > 0.0f ? 1.0f / dyn : 0.0f;
-        };
-        keep(g, 0);
-        keep(u, 1);
-      }
+        for (int e = 0; e < 8; ++e) c[e] = sat_code(x[e] * dyn);
+        const u32x2 v = {pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7])};
+        __builtin_nontemporal_store(v, (u32x2 *)(a.codes + r * 2 * I + half * I + col));
+        if (sub == 0) a.scales[(r * 2 + half) * nb + b] = m > 0.0f ? 1.0f / dyn : 0.0f;
+      };
+      keep(g, 0);
+      keep(u, 1);
     }
   }
 }
 
-// ---- backward: L threads a row ------------------------------------------------------------------------
+// ---- backward: L threads a row, U chunks of 8 columns a thread at a time -------------------------------
 __device__ __forceinline__ void unpack_codes(u32x2 v, float scale, float *f) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[e] = (float)((int)(v[e >> 2] << (24 - 8 * (e & 3))) >> 24) * scale;
 }
 
-template <int L, bool KEPT>
+template <int L, int U, bool KEPT>
 __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
+  constexpr int R = 256 / L, W = L > 64 ? L / 64 : 1;  // rows of a workgroup, waves of a row
   __shared__ float red[2][4];
   int par = 0;
   const int lane = threadIdx.x % L, I = a.I, nch = I >> 3;
   const uint32_t nb = (uint32_t)(I + 127) / 128;
-  constexpr int R = 256 / L;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R) {
     const int64_t r = r0 + threadIdx.x / L;
     const bool used = r < a.rows && row_used(a.g, r);
     float dot = 0.0f;
     if (used) {
       const float w = a.w ? a.w[r] : 1.0f;
-      for (int c = lane; c < nch; c += L) {
-        float g[8], u[8], d[8], dg[8], du[8], h[8];
-        unpack8(((const u32x4 *)(a.go + r * I))[c], d);
-        if constexpr (KEPT) {
-          const int8_t *p = a.codes + r * 2 * I + c * 8;
-          const float *s = a.scales + r * 2 * nb + (c >> 4);
-          unpack_codes(*(const u32x2 *)p, s[0], g);
-          unpack_codes(*(const u32x2 *)(p + I), s[nb], u);
-        } else {
-          const uint16_t *p = a.h0 + r * 2 * I + c * 8;
-          unpack8(*(const u32x4 *)p, g);
-          unpack8(*(const u32x4 *)(p + I), u);
+      for (int c0 = lane; c0 < nch; c0 += L * U) {
+        u32x4 dv[U], gv[U], uv[U];
+        u32x2 gc[U], uc[U];
+        float gs[U], us[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          const int c = c0 + k * L < nch ? c0 + k * L : c0;
+          dv[k] = ((const u32x4 *)(a.go + r * I))[c];
+          if constexpr (KEPT) {
+            const int8_t *p = a.codes + r * 2 * I + c * 8;
+            const float *s = a.scales + r * 2 * nb + (c >> 4);
+            gc[k] = *(const u32x2 *)p;
+            uc[k] = *(const u32x2 *)(p + I);
+            gs[k] = s[0];
+            us[k] = s[nb];
+          } else {
+            const uint16_t *p = a.h0 + r * 2 * I + c * 8;
+            gv[k] = *(const u32x4 *)p;
+            uv[k] = *(const u32x4 *)(p + I);
+          }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const Logistic s = logistic(g[e]);
-          const float wd = w * d[e], act = s.s1 * g[e];
-          du[e] = act * wd * s.s2;
-          dg[e] = s.s1 * u[e] * wd * s.s2 * __builtin_fmaf(g[e], s.rest, 1.0f);
-          const float hu = act * u[e] * s.s2;
-          h[e] = hu * w;
-          dot = __builtin_fmaf(d[e], hu, dot);
+        for (int k = 0; k < U; ++k) {
+          const int c = c0 + k * L;
+          if (c >= nch) continue;
+          float g[8], u[8], d[8], dg[8], du[8], h[8];
+          unpack8(dv[k], d);
+          if constexpr (KEPT) {
+            unpack_codes(gc[k], gs[k], g);
+            unpack_codes(uc[k], us[k], u);
+          } else {
+            unpack8(gv[k], g);
+            unpack8(uv[k], u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const Logistic s = logistic(g[e]);
+            const float wd = w * d[e], act = s.s1 * g[e];
+            du[e] = act * wd * s.s2;
+            dg[e] = s.s1 * u[e] * wd * s.s2 * __builtin_fmaf(g[e], s.rest, 1.0f);
+            const float hu = act * u[e] * s.s2;
+            h[e] = hu * w;
+            dot = __builtin_fmaf(d[e], hu, dot);
+          }
+          if (a.gh0) {
+            u32x4 *p = (u32x4 *)(a.gh0 + r * 2 * I + c * 8);
+            __builtin_nontemporal_store(pack8(dg), p);
+            __builtin_nontemporal_store(pack8(du), p + nch);
+          }
+          if (a.out) __builtin_nontemporal_store(pack8(h), (u32x4 *)(a.out + r * I) + c);
         }
-        if (a.gh0) {
-          *(u32x4 *)(a.gh0 + r * 2 * I + c * 8) = pack8(dg);
-          *(u32x4 *)(a.gh0 + r * 2 * I + I + c * 8) = pack8(du);
-        }
-        if (a.out) *(u32x4 *)(a.out + r * I + c * 8) = pack8(h);
       }
     }
     if (a.gw) {
 #pragma unroll
       for (int s = (L < 64 ? L : 64) / 2; s > 0; s >>= 1) dot += __shfl_xor(dot, s);
-      if constexpr (L > 64) {
+      if constexpr (W > 1) {
         if ((threadIdx.x & 63) == 0) red[par][threadIdx.x >> 6] = dot;
         __syncthreads();
-        dot = (red[par][0] + red[par][1]) + (red[par][2] + red[par][3]);
+        dot = red[par][threadIdx.x / L * W];
+#pragma unroll
+        for (int v = 1; v < W; ++v) dot += red[par][threadIdx.x / L * W + v];
         par ^= 1;
       }
       if (used && lane == 0) a.gw[r] = dot;
@@ -171,8 +184,7 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
 
 hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  const uint64_t blocks = (uint64_t)a.rows * ((a.I + 127) / 128);
-  const uint64_t wg = (blocks + 16 * kFwdBlocks - 1) / (16 * kFwdBlocks);
+  const uint64_t wg = ((uint64_t)a.rows * ((a.I + 127) / 128) + 15) / 16;
   const dim3 grid((unsigned)(wg < kMostGroups ? wg : kMostGroups)), block(256);
   if (a.codes) hipLaunchKernelGGL((swiglu_kernel<true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((swiglu_kernel<false>), grid, block, 0, st, a);
@@ -183,15 +195,28 @@ template <int L>
 static void launch_grad(const SwigluArgs &a, hipStream_t st) {
   const uint64_t wg = ((uint64_t)a.rows + 256 / L - 1) / (256 / L);
   const dim3 grid((unsigned)(wg < kMostGroups ? wg : kMostGroups)), block(256);
-  if (a.codes) hipLaunchKernelGGL((swiglu_grad_kernel<L, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((swiglu_grad_kernel<L, false>), grid, block, 0, st, a);
+  if (a.codes) hipLaunchKernelGGL((swiglu_grad_kernel<L, 2, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((swiglu_grad_kernel<L, 1, false>), grid, block, 0, st, a);
 }
 
+// Threads a row: as many as keep each busy, with two chunks from codes (which are half as wide: a wave has too little under
+// way with one), with one from bf16.  us, from codes / from bf16, by threads a row:
+//                          16           32           64          128          256
+//   65536 rows of  256   36 / 38      47 / 42      81 / 55     126 / 87     218 / 155
+//   32768 rows of  512   36 / 39      35 / 38      47 / 37      72 / 50     118 / 85
+//   30000 rows of 1024   61 / 72      57 / 66      59 / 64      82 / 63     127 / 91
+//   32768 rows of 2048  161 / 202    132 / 163    118 / 148    122 / 135    173 / 132
+//    6168 rows of 2056   55 / 63      46 / 52      34 / 40      32 / 34      41 / 33
+//    8192 rows of 4096   77 / 95      73 / 84      66 / 76      63 / 75      64 / 70
+//     100 rows of 8192   42 / 56      25 / 30      14 / 16     8.8 / 9.7    6.2 / 6.7
 hipError_t launch_swiglu_grad(const SwigluArgs &a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  if (a.I <= 128) launch_grad<16>(a, st);
-  else if (a.I <= 1024) launch_grad<64>(a, st);
-  else launch_grad<256>(a, st);
+  const int chunks = a.I / (a.codes ? 16 : 8);
+  if (chunks >= 256) launch_grad<256>(a, st);
+  else if (chunks >= 128) launch_grad<128>(a, st);
+  else if (chunks >= 64) launch_grad<64>(a, st);
+  else if (chunks >= 32) launch_grad<32>(a, st);
+  else launch_grad<16>(a, st);
   return hipGetLastError();
 }
 
