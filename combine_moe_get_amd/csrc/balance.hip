@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
     auto fetch = [&](int64_t tb) {
       const int64_t t = tb + sub;
       const bool on = t < t1 && (!a.mask || a.mask[t]);
-      load_logits<L, NV, F32>(a.logits, t, E, lane, on, next);
+      load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, next);
       next_id = on && lane < K ? a.idx[t * K + lane] : -1;
     };
-    fetch(t0);
+    if (t0 < t1) fetch(t0);
     for (int64_t tb = t0; tb < t1; tb += TOKENS) {  // the same for all lanes of the wave
       float l[NV], p[NV], rest[NV];
 #pragma unroll
@@ -106,14 +106,14 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
 #pragma unroll
       for (int i = 0; i < NV; ++i) sum += p[i];
       sum = sum_of<L>(sum);
-      const float r = counts ? 1.0f / sum : 0.0f;
+      const float r = counts ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(p[i], r, acc[i]);
       if (a.z_coef != 0.0f) {
         if constexpr (SCORE == MOE_SCORE_SIGMOID) {
           sum = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) sum += l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+          for (int i = 0; i < NV; ++i) sum += exp_neg(l[i] - m);
           sum = sum_of<L>(sum);
         }
         const double lse = counts ? m + logf(sum) : 0.0f;
@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
   const int E = a.E, K = a.K;
   const bool losses = a.counts != nullptr, zloss = losses && a.z_coef != 0.0f;
   const float per_balance = losses ? (float)((double)(a.gl ? a.gl[0] : 1.0f) * a.balance_coef * E / ((double)a.S * K)) : 0.0f;
+  const float mean_count = (float)K / (float)E;
   float per_z = 0.0f;  // of a token
   if (zloss) {
     int n = 0;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
     const int64_t t = tb + sub;
     const bool on = t < a.T && (!a.mask || a.mask[t]);
     float l[NV], p[NV], rest[NV], d[NV];
-    load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
+    load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, l);
     int id = on && a.gw && lane < K ? a.idx[t * K + lane] : -1;
     if (id < 0 || id >= E) id = -1;
     float lj = MOE_NEG_INF, gw = 0.0f;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) sum += p[i];
     sum = sum_of<L>(sum);
-    const float r = counts ? 1.0f / sum : 0.0f;
+    const float r = counts ? __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       p[i] *= r;
@@ -380,18 +381,16 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
     }
     if (a.gw) {
       // of the logarithms of the scores of the token's ids: slot j on lane j
-      float aj, sum_a = 0.0f;
+      float aj, sum_a = 0.0f, s, s_rest;
       if (a.renorm) {
-        const float q = !some ? MOE_NEG_INF : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
-        const float mq = max_of<L>(q);
-        float w = some ? exp_neg(q - mq) : 0.0f;
-        const float all = sum_of<L>(w);
-        w = some ? w / all : 0.0f;
+        scores<1, SCORE>(&lj, max_of<L>(lj), &s, &s_rest);
+        const float all = sum_of<L>(some ? s : 0.0f);
+        const float w = some ? s * __builtin_amdgcn_rcpf(all) : 0.0f;
         const float mean = sum_of<L>(w * gw);
         aj = a.scale * w * (gw - mean);
       } else {
-        const float s = !some ? 0.0f : SCORE == MOE_SCORE_SOFTMAX ? exp_neg(lj - m) * r : 1.0f / (1.0f + expf(-lj));
-        aj = a.scale * s * gw;
+        s = SCORE == MOE_SCORE_SOFTMAX ? exp_neg(lj - m) * r : sigmoid(lj, s_rest);
+        aj = some ? a.scale * s * gw : 0.0f;
         if (SCORE == MOE_SCORE_SOFTMAX) sum_a = sum_of<L>(aj);
       }
       // to the lanes that hold the ids, through LDS; slots of the same id all carry their sum
@@ -423,8 +422,8 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
     if (losses) {
       const uint32_t g = on ? (uint32_t)t / n : 0;
       const int live = a.tokens[g];
-      const float f = live > 0 ? per_balance / (float)live / (float)live : 0.0f;
-      const float c0 = (float)K * (float)live / (float)E;  // sum p = 1: any constant may be taken off; the mean loses least
+      const float over = live > 0 ? __builtin_amdgcn_rcpf((float)live) : 0.0f, f = per_balance * over * over;
+      const float c0 = mean_count * (float)live;  // sum p = 1: any constant may be taken off; the mean loses least
       float A[NV], s = 0.0f;
       const int32_t *ct = a.counts + (int64_t)g * E;
       int c[NV];
@@ -442,12 +441,12 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {  // behind the last id p is 0
-        A[i] = f * ((float)c[i] - c0);
+        A[i] = (float)c[i] - c0;
         s = __builtin_fmaf(A[i], p[i], s);
       }
       s = sum_of<L>(s);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(p[i], A[i] - s, d[i]);
+      for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(p[i] * f, A[i] - s, d[i]);
     }
     if constexpr (SCORE == MOE_SCORE_SIGMOID) {
 #pragma unroll
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
         sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          e[i] = l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+          e[i] = exp_neg(l[i] - m);
           sum += e[i];
         }
         sum = sum_of<L>(sum);
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
       const float lse = counts ? m + logf(sum) : 0.0f;
       const float f = counts ? per_z * lse : 0.0f;
       if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-        const float fr = counts ? f / sum : 0.0f;
+        const float fr = counts ? f * __builtin_amdgcn_rcpf(sum) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(fr, e[i], d[i]);
       } else {

@@ -3,19 +3,16 @@
 
 namespace moe {
 
-// A key to compare by: in 64 bits, its last 11 replaced by the id, so that no two of a token's are the same and the lower id
-// is the larger of two that were.  An fp32 logit keeps all its bits; a score keeps 42.
+// A logit to compare by, its id in the last 11 bits of a double: no two of a token's are the same, and the lower id is the
+// larger of two that were.  An fp32 value leaves 29 bits free.
 constexpr uint32_t kTag = 2047;
-__device__ __forceinline__ double tagged(double key, int id) {
+__device__ __forceinline__ double tagged(float logit, int id) {
+  const double key = (double)(logit + 0.0f);  // one zero
   const int hi = __double2hiint(key);
-  const uint32_t tag = (uint32_t)id ^ (hi < 0 ? 0u : kTag);
-  return __hiloint2double(hi, (int)(((uint32_t)__double2loint(key) & ~kTag) | tag));
+  return __hiloint2double(hi, __double2loint(key) | (int)((uint32_t)id ^ (hi < 0 ? 0u : kTag)));
 }
 __device__ __forceinline__ int id_in(double key) {
   return (int)(((uint32_t)__double2loint(key) & kTag) ^ (__double2hiint(key) < 0 ? 0u : kTag));
-}
-__device__ __forceinline__ double untagged(double key) {
-  return __hiloint2double(__double2hiint(key), (int)((uint32_t)__double2loint(key) & ~kTag));
 }
 
 // the two best of (a, b) and (c, d), each pair in order
@@ -77,68 +74,52 @@ template <int L>
 struct RouteLds {
   static constexpr int CANDIDATES = 4 * L;
   __align__(16) double cand[CANDIDATES + 4];
+  int ids[CANDIDATES + 4];
   double best[16];
 };
 
-// The groups that a token's ids may come from (bit g), by scores in 64 bits: value(i) as in group_best, tagged.
+// The groups that a token's ids may come from (bit g), by scores in 64 bits: value(i) as in group_best.
 template <int L, int NV, class Value>
 __device__ __forceinline__ uint64_t groups_wide(const RouteArgs &a, int lane, double *gs, Value value) {
   const double none = (double)MOE_NEG_INF;
   group_best<L, NV>(a, lane, none, value, [&](double one, double two, int g) {
-    if (a.two && two > none) one = untagged(one) + untagged(two);
-    gs[g] = a.two && one > none ? tagged(fmin(one, DBL_MAX), g) : one;
+    gs[g] = a.two && two > none ? fmin(one + two, DBL_MAX) : one;
   });
   lds_order();
   uint64_t kept = 0;
   for (int g0 = 0; g0 < a.G; g0 += L) {
-    const double mine = g0 + lane < a.G ? gs[g0 + lane] : none;
+    const int g = g0 + lane;
+    const double mine = g < a.G ? gs[g] : none;
     int better = 0;
-    for (int o = 0; o < a.G; ++o) better += gs[o] > mine;
+    for (int o = 0; o < a.G; ++o) better += gs[o] > mine || (gs[o] == mine && o < g);
     kept |= token_bits<L>(ballot(mine > none && better < a.keep)) << g0;
   }
   lds_order();
   return kept;
 }
 
-// The best K by rounds, each the best of the lanes' best, in 64 bits: on lane j the key of slot j, or none.  A lane holds its
-// three best in order; one that gave all three looks for the next ones below the last.
+// The best K by rounds, each the best of what comes behind the last round's: the id of slot j on lane j, or -1.  key(i): in 64
+// bits, of the lane's i-th id.
 template <int L, int NV, class Key>
-__device__ __forceinline__ double choose_by_rounds(int K, int lane, Key key) {
+__device__ __forceinline__ int choose_by_rounds(int K, int lane, Key key) {
   const double none = (double)MOE_NEG_INF;
-  double b0, b1, b2, mine = none;
-  auto look = [&](double below) {
-    b0 = b1 = b2 = none;
+  double last = (double)__builtin_inf();
+  int last_id = -1, mine = -1;
+  for (int j = 0; j < K; ++j) {
+    double best = none;
+    int id = 1 << 30;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const double any = key(i), k = any < below ? any : none;
-      const double k1 = fmin(b0, k);
-      b0 = fmax(b0, k);
-      const double k2 = fmin(b1, k1);
-      b1 = fmax(b1, k1);
-      b2 = fmax(b2, k2);
+      const double k = key(i);
+      const int e = id_of<L>(lane, i);
+      if ((k < last || (k == last && e > last_id)) && (k > best || (k == best && e < id))) {
+        best = k;
+        id = e;
+      }
     }
-  };
-  look((double)__builtin_inf());
-  int taken = 0;
-  for (int j = 0; j < K; ++j) {
-    const double top = max_of<L>(b0);
-    if (lane == j) mine = top;
-    const bool hit = b0 == top && top > none;
-    if (hit) {
-      b0 = b1;
-      b1 = b2;
-      b2 = none;
-      ++taken;
-    }
-    if (ballot(hit && taken == 3)) {
-      const bool empty = hit && taken == 3;
-      const double o0 = b0, o1 = b1, o2 = b2;
-      look(top);
-      b0 = empty ? b0 : o0;
-      b1 = empty ? b1 : o1;
-      b2 = empty ? b2 : o2;
-      taken = empty ? 0 : taken;
-    }
+    last = max_of<L>(best);
+    last_id = fold<L>(best == last ? id : 1 << 30, [](int x, int y) { return x < y ? x : y; });
+    if (lane == j && last > none) mine = last_id;
   }
   return mine;
 }
@@ -156,16 +137,16 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   const double none = (double)MOE_NEG_INF;
   const float nonef = MOE_NEG_INF;
   float l[NV];
-  load_logits<L, NV, F32>(a.logits, t, E, lane, on, l);
+  load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, l);
 
   // What the formulas of softmax need of the whole row: its largest logit, the sum of exponentials.
   float m = 0.0f, sum = 1.0f;
   double whole = 1.0;
-  if (SCORE == MOE_SCORE_SOFTMAX ? BIAS || (grouped && a.two) || !a.renorm : BIAS || (grouped && a.two)) m = row_max<L, NV>(l);
+  if (SCORE == MOE_SCORE_SOFTMAX && (BIAS || (grouped && a.two) || !a.renorm)) m = row_max<L, NV>(l);
   if (SCORE == MOE_SCORE_SOFTMAX && !a.renorm) {
     sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sum += l[i] > nonef ? exp_neg(l[i] - m) : 0.0f;
+    for (int i = 0; i < NV; ++i) sum += exp_neg(l[i] - m);
     sum = sum_of<L>(sum);
   }
   if (SCORE == MOE_SCORE_SOFTMAX && BIAS) {
@@ -181,9 +162,9 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   };
   auto key_of = [&](float v, int id) -> double {
     if (!(v > nonef)) return none;
-    if (!BIAS) return tagged((double)(v + 0.0f), id);  // one zero
+    if (!BIAS) return tagged(v, id);
     const float b = a.bias[id];
-    return b > nonef ? tagged(fmin(score(v) + (double)b, DBL_MAX), id) : none;
+    return b > nonef ? fmin(score(v) + (double)b, DBL_MAX) : none;
   };
 
   // Keys in 32 bits: logits as they are; scores, at most 1, are good to 2^-22, and with a bias the sum to 2^-24 of itself.
@@ -191,9 +172,11 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   float k[NV];
   if constexpr (BIAS) {
     float rest[NV];
-    scores<NV, SCORE>(l, m, k, rest);
-    const bool low = SCORE == MOE_SCORE_SIGMOID && m < -60.0f;  // scores<> took a factor out
-    const float f = SCORE == MOE_SCORE_SOFTMAX ? (float)whole : low ? 0.0f : 1.0f;
+    if (SCORE == MOE_SCORE_SOFTMAX) scores<NV, SCORE>(l, m, k, rest);
+    else
+#pragma unroll
+      for (int i = 0; i < NV; ++i) k[i] = sigmoid(l[i], rest[i]);
+    const float f = (float)whole;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int id = id_of<L>(lane, i);
@@ -216,9 +199,11 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     };
     if (!BIAS && a.two) {
       float s[NV], rest[NV];
-      scores<NV, SCORE>(l, m, s, rest);
-      const bool low = SCORE == MOE_SCORE_SIGMOID && m < -60.0f;
-      group_best<L, NV>(a, lane, nonef, [&](int i) { return l[i] > nonef ? (low ? 0.0f : s[i]) : nonef; }, bounds);
+      if (SCORE == MOE_SCORE_SOFTMAX) scores<NV, SCORE>(l, m, s, rest);
+      else
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s[i] = sigmoid(l[i], rest[i]);
+      group_best<L, NV>(a, lane, nonef, [&](int i) { return l[i] > nonef ? s[i] : nonef; }, bounds);
     } else {
       group_best<L, NV>(a, lane, nonef, [&](int i) { return k[i]; }, bounds);
     }
@@ -250,7 +235,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     if (ballot(open))  // two groups too near one another at the border: some of 10^5 tokens
       kept = groups_wide<L, NV>(a, lane, my.cand, [&](int i) {
         const int id = id_of<L>(lane, i);
-        return BIAS ? key_of(l[i], id) : l[i] > nonef ? tagged(score(l[i]), id) : none;
+        return BIAS ? key_of(l[i], id) : l[i] > nonef ? score(l[i]) : none;
       });
     if (a.span) {
 #pragma unroll
@@ -297,45 +282,54 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   const int before = first ? last : 0;  // in the wave's other tokens
   int at = upto - n - before;
   n = __shfl(upto, L - 1, L) - before;
-  double mine = none;
+  int id = -1;  // of slot `lane`
+  float lj = 0.0f;
   if (ballot(n > RouteLds<L>::CANDIDATES)) {  // rows of one value, or nearly
-    mine = choose_by_rounds<L, NV>(K, lane, [&](int i) { return key_of(l[i], id_of<L>(lane, i)); });
+    id = choose_by_rounds<L, NV>(K, lane, [&](int i) { return key_of(l[i], id_of<L>(lane, i)); });
+    if (id >= 0) lj = logit_at(a.logits, F32, t * E + id);
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (k[i] >= bound) my.cand[at++] = __hiloint2double(__float_as_int(l[i]), id_of<L>(lane, i));
     lds_order();
     for (int c = lane; ballot(c < n); c += L)
-      if (c < n) my.cand[c] = key_of(__int_as_float(__double2hiint(my.cand[c])), __double2loint(my.cand[c]));
+      if (c < n) {
+        const int e = __double2loint(my.cand[c]);
+        my.cand[c] = key_of(__int_as_float(__double2hiint(my.cand[c])), e);
+        if (BIAS) my.ids[c] = e;
+      }
     if (lane < 4) my.cand[n + lane] = none;
     lds_order();
     for (int c = lane; ballot(c < n); c += L) {
       const double key = c < n ? my.cand[c] : none;
+      const int e = BIAS && c < n ? my.ids[c] : 0;
       int r = 0;
       for (int o = 0; o < n; o += 4)
-        r += (my.cand[o] > key) + (my.cand[o + 1] > key) + (my.cand[o + 2] > key) + (my.cand[o + 3] > key);
-      if (key > none && r < K) my.best[r] = key;
+#pragma unroll
+        for (int q = o; q < o + 4; ++q) r += my.cand[q] > key || (BIAS && my.cand[q] == key && my.ids[q] < e);
+      if (key > none && r < K) my.best[r] = BIAS ? (double)e : key;
     }
     lds_order();
-    if (lane < K) mine = my.best[lane];
+    const double best = lane < K ? my.best[lane] : none;
+    if (best > none) {
+      id = BIAS ? (int)best : id_in(best);
+      lj = BIAS ? logit_at(a.logits, F32, t * E + id) : (float)best;  // the tag is far below the last bit of 32
+    }
   }
+  const bool some = id >= 0;
 
-  const bool some = mine > none;
-  const int id = some ? id_in(mine) : -1;
-  // without a bias the key is the logit, its tag far below the last bit of 32
-  const float lj = !some ? 0.0f : BIAS ? logit_at(a.logits, F32, t * E + id) : (float)mine;
-  float w;
+  float w, rest;
   if (a.renorm) {
-    const float q = !some ? nonef : SCORE == MOE_SCORE_SOFTMAX ? lj : log_sigmoid(lj);
-    const float mq = max_of<L>(q);
-    w = some ? exp_neg(q - mq) : 0.0f;
+    const float lw = some ? lj : nonef;
+    scores<1, SCORE>(&lw, max_of<L>(lw), &w, &rest);
+    w = some ? w : 0.0f;
     const float all = sum_of<L>(w);
-    w = some ? w / all * a.scale : 0.0f;
-  } else if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-    w = some ? exp_neg(lj - m) / sum * a.scale : 0.0f;
+    w = some ? w / all : 0.0f;
   } else {
-    w = some ? 1.0f / (1.0f + expf(-lj)) * a.scale : 0.0f;
+    w = SCORE == MOE_SCORE_SOFTMAX ? exp_neg(lj - m) / sum : sigmoid(lj, rest);
+    w = some ? w : 0.0f;
   }
+  w *= a.scale;
   if (t < a.T && lane < K) {
     a.idx[t * K + lane] = id;
     a.w[t * K + lane] = w;

@@ -134,17 +134,17 @@ __device__ __forceinline__ int id_of(int lane, int i) {
   return ((i >> 2) * L + lane) * 4 + (i & 3);
 }
 
-// A lane's logits of token t; -inf where there is none (`on`: whether the token counts).  Rows of a multiple of four ids are
-// read four at a time.
+// A lane's logits of token t of T; -inf where there is none (`on`: whether the token counts).  Rows of a multiple of four ids
+// are read four at a time.  Others one at a time, also where there is none (the row's last is read again): branches around
+// each would cost more.
 template <int L, int NV, bool F32>
-__device__ __forceinline__ void load_logits(const void *logits, int64_t t, int E, int lane, bool on, float *l) {
-  const bool wide = (E & 3) == 0;
+__device__ __forceinline__ void load_logits(const void *logits, int64_t t, int T, int E, int lane, bool on, float *l) {
+  if ((E & 3) == 0) {
 #pragma unroll
-  for (int c = 0; c < NV / 4; ++c) {
-    const int e = id_of<L>(lane, c * 4);
-    float *v = l + c * 4;
-    v[0] = v[1] = v[2] = v[3] = MOE_NEG_INF;
-    if (wide) {
+    for (int c = 0; c < NV / 4; ++c) {
+      const int e = id_of<L>(lane, c * 4);
+      float *v = l + c * 4;
+      v[0] = v[1] = v[2] = v[3] = MOE_NEG_INF;
       if (on && e < E) {
         if constexpr (F32) {
           const f32x4 x = *(const f32x4 *)((const float *)logits + t * E + e);
@@ -156,13 +156,16 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t t, int E
           for (int k = 0; k < 4; ++k) v[k] = k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
         }
       }
-    } else {
+    }
+  } else {
+    const int64_t row = (t < T ? t : T - 1) * E;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (on && e + k < E) {
-          if constexpr (F32) v[k] = ((const float *)logits)[t * E + e + k];
-          else v[k] = __uint_as_float((uint32_t)((const uint16_t *)logits)[t * E + e + k] << 16);
-        }
+    for (int i = 0; i < NV; ++i) {
+      const int e = id_of<L>(lane, i), at = e < E ? e : E - 1;
+      float v;
+      if constexpr (F32) v = ((const float *)logits)[row + at];
+      else v = __uint_as_float((uint32_t)((const uint16_t *)logits)[row + at] << 16);
+      l[i] = on && e < E ? v : MOE_NEG_INF;
     }
   }
 #pragma unroll
@@ -177,8 +180,8 @@ __device__ __forceinline__ float row_max(const float *l) {
   return max_of<L>(m);
 }
 
-// exp(x) for x <= 0 (-inf and below -200: 0), good to some two steps of fp32: 2^t of t = x log2(e) rounded, and the rest of
-// the product as a factor
+// exp(x) for x <= 0 (below -200, -inf and NaN: 0), good to some two steps of fp32: 2^t of t = x log2(e) rounded, and the rest
+// of the product as a factor
 __device__ __forceinline__ float exp_neg(float x) {
   const float c = fmaxf(x, -200.0f);
   const float t = c * 1.44269502e+00f;
@@ -187,28 +190,29 @@ __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_fmaf(e * 0.693147182f, r, e);
 }
 
-// The scores of a token's logits up to a common factor, s, and for sigmoids 1 - sigmoid, rest.  m: its largest logit.
-// Softmax: exp(l - m).  Sigmoid: with e = exp(-|l|), e / (1 + e) or 1 / (1 + e); of a token with no logit above -60 divided
-// by exp(m), so that they do not vanish.  0 where there is no logit.
+// 1 / (1 + exp(-l)) and 1 minus it, for l that is not -inf or where neither is used
+__device__ __forceinline__ float sigmoid(float l, float &rest) {
+  const float e = exp_neg(-fabsf(l)), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+  rest = l > 0.0f ? er : r;
+  return l > 0.0f ? r : er;
+}
+
+// The scores of some of a token's logits up to a common factor, s, and for sigmoids 1 - sigmoid, rest.  m: the largest of them.
+// Softmax: exp(l - m).  Sigmoid: where no logit is above -60 divided by exp(m), so that they do not vanish.  s is 0 where
+// there is no logit (also where there is none at all).
 template <int NV, int SCORE>
 __device__ __forceinline__ void scores(const float *l, float m, float *s, float *rest) {
   if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = l[i] > MOE_NEG_INF ? exp_neg(l[i] - m) : 0.0f;
+    for (int i = 0; i < NV; ++i) s[i] = exp_neg(l[i] - m);
   } else {
-    const bool low = m < -60.0f;
-    const float shift = low ? m : 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const float e = exp_neg(-fabsf(l[i] - shift)), r = low ? 1.0f : __builtin_amdgcn_rcpf(1.0f + e);
-      s[i] = l[i] > 0.0f ? r : e * r;
-      rest[i] = l[i] > 0.0f ? e * r : r;
-      if (!(l[i] > MOE_NEG_INF)) s[i] = rest[i] = 0.0f;
+    for (int i = 0; i < NV; ++i) s[i] = sigmoid(l[i], rest[i]);
+    if (ballot(m < -60.0f)) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[i] = m < -60.0f ? exp_neg(l[i] - m) : s[i];
     }
   }
 }
-
-// the logarithm of a sigmoid
-__device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.0f) - log1pf(expf(-fabsf(l))); }
 
 }  // namespace moe

@@ -63,7 +63,8 @@ def some_ids(r, l, K, dropped=0.0):
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("T,E,K,S", [(1, 1, 1, 1), (1, 8, 2, 1), (3, 7, 3, 3), (130, 33, 4, 2), (64, 64, 16, 8), (6, 65, 1, 1),
                                      (96, 128, 6, 4), (77, 134, 6, 7), (512, 256, 8, 2), (12, 257, 5, 3), (36, 512, 8, 1),
-                                     (20, 1000, 8, 4), (24, 2048, 16, 2), (5000, 40, 2, 1)])
+                                     (20, 1000, 8, 4), (24, 2048, 16, 2), (5000, 40, 2, 1), (8192, 100, 3, 4), (8300, 128, 8, 1),
+                                     (40, 1022, 3, 1), (700, 1024, 8, 2), (300, 2047, 8, 1)])
 def test_against_the_definitions(T, E, K, S, bf16, renorm, score):
     print(f"[balance] {T} {E} {K} {S} {bf16} {renorm} {score}", flush=True)
     r = np.random.default_rng([T, E, K, S])
@@ -160,13 +161,15 @@ def test_segments_without_a_live_token_and_no_tokens():
     assert b.segment_tokens.tolist() == [4, 0, 4] and bool((b.prob_sums[1] == 0).all())
     b, g = run(l, ids, mg.SCORE_SIGMOID, gw=r.standard_normal((12, 2)), S=3, zc=0.2, mask=np.zeros(12, np.uint8))
     assert b.losses.tolist() == [0, 0] and bool((g == 0).all())
-    s = mg.make_route_shape(0, 16, 2)
-    bal = mg.make_balance(2, 1.0, 1.0)
-    e = torch.empty(0, 16, device=X.DEV)
-    i = torch.empty(0, 2, dtype=torch.int32, device=X.DEV)
-    b = mg.balance_loss(s, bal, e, i)
-    assert b.losses.tolist() == [0, 0] and bool((b.counts == 0).all()) and b.segment_tokens.tolist() == [0, 0]
-    assert mg.route_grad(s, e, i, torch.empty(0, 2, device=X.DEV), bal, b).shape == (0, 16)
+    for E in (16, 18, 130, 1026):
+        s = mg.make_route_shape(0, E, 2)
+        bal = mg.make_balance(2, 1.0, 1.0)
+        e = torch.empty(0, E, device=X.DEV)
+        i = torch.empty(0, 2, dtype=torch.int32, device=X.DEV)
+        b = mg.balance_loss(s, bal, e, i)
+        assert b.losses.tolist() == [0, 0] and bool((b.counts == 0).all()) and b.segment_tokens.tolist() == [0, 0]
+        assert bool((b.prob_sums == 0).all())
+        assert mg.route_grad(s, e, i, torch.empty(0, 2, device=X.DEV), bal, b).shape == (0, E)
 
 
 def test_many_segments():

@@ -123,6 +123,60 @@ def test_logits_that_are_no_numbers(score, renorm, bf16):
     assert not np.isin(ids, [0, 1]).any() and ids[7, 0] != 2 and ids[9, 0] == 2 and ids[9, 1] == 5
 
 
+@pytest.mark.parametrize("T,E,K,groups,keep", [(8200, 100, 6, 1, 1), (8192, 128, 8, 8, 3), (9000, 65, 16, 5, 2)])
+def test_many_tokens(T, E, K, groups, keep):
+    r = np.random.default_rng([T, E])
+    mask = (r.random(T) < 0.9).astype(np.uint8)
+    check(logits(r, T, E, bf16=True), K, mg.SCORE_SIGMOID, groups=groups, keep=keep, two=True, mask=mask)
+    check(logits(r, T, E), K, mg.SCORE_SOFTMAX, groups=groups, keep=keep, bias=(0.1 * r.standard_normal(E)).astype(np.float32))
+
+
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,K", [(64, 8), (128, 16), (256, 8), (512, 8), (1024, 16), (2048, 16)])
+def test_rows_with_many_near_the_best(E, K, biased):
+    """The best ids lie together in few lanes, or many ids share the best values: from a handful of candidates to all ids."""
+    r = np.random.default_rng([E, K, biased])
+    bias = (2.0 ** -26 * r.integers(0, 4, E)).astype(np.float32) if biased else None
+    rows = []
+    for width in (1, 3, K - 1, K, K + 1, 17, 33, 60, 64, 65, 130, 260, E):
+        for first in (0, E - min(width, E), r.integers(0, E)):
+            l = r.standard_normal(E) - 8
+            at = (first + np.arange(min(width, E))) % E
+            rows.append(l.copy())
+            rows[-1][at] = 3.0                                            # ties
+            rows.append(l.copy())
+            rows[-1][at] = 3.0 + 0.01 * r.permutation(len(at))            # in any order
+            rows.append(l.copy())
+            rows[-1][at] = 3.0 + 2.0 ** -22 * r.permutation(len(at))      # neighbours in fp32
+    l = torch.from_numpy(np.array(rows, np.float32))
+    for score in (mg.SCORE_SOFTMAX, mg.SCORE_SIGMOID):
+        check(l, K, score, bias=bias)
+        check(l, K, score, bias=bias, groups=8, keep=5, two=True)
+
+
+@pytest.mark.parametrize("score", [mg.SCORE_SOFTMAX, mg.SCORE_SIGMOID])
+@pytest.mark.parametrize("E,G", [(64, 8), (256, 8), (96, 3), (512, 4)])
+def test_groups_next_to_one_another(E, G, score):
+    """Group scores that differ by some 1e-9, which 32 bits do not hold, tie, or are set apart by a bias of any size."""
+    r = np.random.default_rng([E, G])
+    T, per, keep, K = 64, E // G, max(1, G // 2), 4
+    l = r.standard_normal((T, E)) - 3
+    for t in range(T):
+        for g in range(G):
+            at = g * per + r.permutation(per)[:2]
+            l[t, at] = [1.5, 1.0 + 2.0 ** -23 * r.integers(0, 3)]
+    l = torch.from_numpy(l.astype(np.float32))
+    check(l, K, score, groups=G, keep=keep, two=True)
+    check(l, K, score, groups=G, keep=keep, two=True, bias=(2.0 ** -28 * r.integers(0, 8, E)).astype(np.float32))
+    check(l, K, score, groups=G, keep=keep, two=False, bias=(2.0 ** -28 * r.integers(0, 8, E)).astype(np.float32))
+    bias = (0.1 * r.standard_normal(E)).astype(np.float32)
+    bias[[0, 5, per, E - 1]] = [3.0e38, -3.0e38, INF, -1e20]
+    for two in (False, True):
+        check(l, K, score, groups=G, keep=keep, two=two, bias=bias)
+    bias[:] = -3.4e38
+    check(l, K, score, groups=G, keep=keep, two=False, bias=bias)
+
+
 def test_near_scores_are_told_apart():
     """Sigmoids of neighbouring fp32 logits, and sums with a bias that differ by less than fp32 holds."""
     r = np.random.default_rng(8)
