@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
   __shared__ double zs[TOKENS];
   __shared__ int lives[TOKENS];
   const int lane = threadIdx.x & (L - 1), sub = threadIdx.x / L;
+  const int wave0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (64 / L);  // the wave's first token
   const int E = a.E, K = a.K, n = a.T / a.S, s = ALONE ? 0 : blockIdx.x % slices;
   double loss = 0.0, all_z = 0.0;  // ALONE: of this thread's columns; of all tokens
   int all_live = 0;
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
     auto fetch = [&](int64_t tb) {
       const int64_t t = tb + sub;
       const bool on = t < t1 && (!a.mask || a.mask[t]);
-      load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, next);
+      load_logits<L, NV, F32>(a.logits, tb + wave0, a.T, E, lane, on, next);
       next_id = on && lane < K ? a.idx[t * K + lane] : -1;
     };
     if (t0 < t1) fetch(t0);
@@ -301,26 +302,29 @@ hipError_t launch_balance(const BalanceArgs &a, int score, bool fp32, hipStream_
 // ---- the gradient --------------------------------------------------------------------------------
 
 template <int L, int NV, bool F32>
-__device__ __forceinline__ void store_grad(void *out, int64_t t, int E, int lane, const float *d) {
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-  const bool wide = (E & 3) == 0;
+__device__ __forceinline__ void store_grad(void *out, int64_t t0, int T, int E, int lane, const float *d) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  constexpr int SIZE = F32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t rows = wave_rows<L>(out, t0, T, E, SIZE);
+  const int off = ((int)(threadIdx.x & 63) / L * E + lane * 4) * SIZE;
 #pragma unroll
   for (int c = 0; c < NV / 4; ++c) {
-    const int e = id_of<L>(lane, c * 4);
     const float *v = d + c * 4;
-    const bf16x4 h = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};  // to nearest even
-    if (wide) {
-      if (e < E) {
-        if constexpr (F32) *(f32x4 *)((float *)out + t * E + e) = f32x4{v[0], v[1], v[2], v[3]};
-        else *(bf16x4 *)((__bf16 *)out + t * E + e) = h;
-      }
+    const int e = id_of<L>(lane, c * 4), at = off + c * L * 4 * SIZE;
+    const bf16x2 h[2] = {{(__bf16)v[0], (__bf16)v[1]}, {(__bf16)v[2], (__bf16)v[3]}};  // to nearest even
+    const u32x2 b = {__builtin_bit_cast(uint32_t, h[0]), __builtin_bit_cast(uint32_t, h[1])};
+    if ((E & 3) == 0) {
+      const int to = e < E ? at : kNowhere;
+      if constexpr (F32)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, rows, to, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b64(b, rows, to, 0, 0);
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (e + k < E) {
-          if constexpr (F32) ((float *)out)[t * E + e + k] = v[k];
-          else ((__bf16 *)out)[t * E + e + k] = h[k];
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int to = e + k < E ? at + k * SIZE : kNowhere;
+        if constexpr (F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[k]), rows, to, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(b[k >> 1] >> (16 * (k & 1))), rows, to, 0, 0);
+      }
     }
   }
 }
@@ -331,6 +335,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
   __shared__ __align__(16) float rows[TOKENS][L * NV];  // what goes to a token's chosen ids
   __shared__ int parts[4];
   const int lane = threadIdx.x & (L - 1), sub = threadIdx.x / L;
+  const int wave0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * (64 / L);  // the wave's first token
   const int E = a.E, K = a.K;
   const bool losses = a.counts != nullptr, zloss = losses && a.z_coef != 0.0f;
   const float per_balance = losses ? (float)((double)(a.gl ? a.gl[0] : 1.0f) * a.balance_coef * E / ((double)a.S * K)) : 0.0f;
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
     const int64_t t = tb + sub;
     const bool on = t < a.T && (!a.mask || a.mask[t]);
     float l[NV], p[NV], rest[NV], d[NV];
-    load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, l);
+    load_logits<L, NV, F32>(a.logits, tb + wave0, a.T, E, lane, on, l);
     int id = on && a.gw && lane < K ? a.idx[t * K + lane] : -1;
     if (id < 0 || id >= E) id = -1;
     float lj = MOE_NEG_INF, gw = 0.0f;
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
     if (losses) {
       const uint32_t g = on ? (uint32_t)t / n : 0;
       const int live = a.tokens[g];
-      const float over = live > 0 ? __builtin_amdgcn_rcpf((float)live) : 0.0f, f = per_balance * over * over;
+      const float over = live > 0 ? __builtin_amdgcn_rcpf((float)live) : 0.0f, f = counts ? per_balance * over * over : 0.0f;
       const float c0 = mean_count * (float)live;  // sum p = 1: any constant may be taken off; the mean loses least
       float A[NV], s = 0.0f;
       const int32_t *ct = a.counts + (int64_t)g * E;
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
         for (int i = 0; i < NV; ++i) d[i] = __builtin_fmaf(f, p[i], d[i]);
       }
     }
-    if (t < a.T) store_grad<L, NV, F32>(a.out, t, E, lane, d);
+    store_grad<L, NV, F32>(a.out, tb + wave0, a.T, E, lane, d);
   }
 }
 

@@ -74,7 +74,7 @@ template <int L>
 struct RouteLds {
   static constexpr int CANDIDATES = 4 * L;
   __align__(16) double cand[CANDIDATES + 4];
-  int ids[CANDIDATES + 4];
+  __align__(16) int ids[CANDIDATES + 4];
   double best[16];
 };
 
@@ -131,13 +131,14 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
   __shared__ RouteLds<L> lds[4 * PER];
   const int lane = threadIdx.x & (L - 1);
   RouteLds<L> &my = lds[threadIdx.x / L];
-  const int64_t t = (int64_t)blockIdx.x * (4 * PER) + threadIdx.x / L;
+  const int64_t t0 = (int64_t)blockIdx.x * (4 * PER) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * PER;  // the wave's first
+  const int64_t t = t0 + (threadIdx.x & 63) / L;
   const int E = a.E, K = a.K;
   const bool on = t < a.T && (!a.mask || a.mask[t]), grouped = a.keep < a.G;
   const double none = (double)MOE_NEG_INF;
   const float nonef = MOE_NEG_INF;
   float l[NV];
-  load_logits<L, NV, F32>(a.logits, t, a.T, E, lane, on, l);
+  load_logits<L, NV, F32>(a.logits, t0, a.T, E, lane, on, l);
 
   // What the formulas of softmax need of the whole row: its largest logit, the sum of exponentials.
   float m = 0.0f, sum = 1.0f;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
       bool in;
       if (exact) {
 #pragma unroll 4
-        for (int o = 0; o < a.G; ++o) above += gs[o] > most || (gs[o] == most && o < g);
+        for (int o = 0; o < a.G; ++o) above += (int)(gs[o] > most) | ((int)(gs[o] == most) & (int)(o < g));
         in = some && above < a.keep;
       } else {
 #pragma unroll 4
@@ -302,11 +303,19 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
     lds_order();
     for (int c = lane; ballot(c < n); c += L) {
       const double key = c < n ? my.cand[c] : none;
-      const int e = BIAS && c < n ? my.ids[c] : 0;
+      const int e = BIAS && c < n ? my.ids[c] : 0;  // without a bias no two keys are the same, and no id is below 0
       int r = 0;
-      for (int o = 0; o < n; o += 4)
-#pragma unroll
-        for (int q = o; q < o + 4; ++q) r += my.cand[q] > key || (BIAS && my.cand[q] == key && my.ids[q] < e);
+      for (int o = 0; o < n; o += 4) {  // four at once, without branches
+        typedef double f64x2 __attribute__((ext_vector_type(2)));
+        typedef int i32x4 __attribute__((ext_vector_type(4)));
+        const f64x2 x = *(const f64x2 *)(my.cand + o), y = *(const f64x2 *)(my.cand + o + 2);
+        i32x4 id4 = {0, 0, 0, 0};
+        if (BIAS) id4 = *(const i32x4 *)(my.ids + o);
+        r += (int)(x[0] > key) | ((int)(x[0] == key) & (int)(id4[0] < e));
+        r += (int)(x[1] > key) | ((int)(x[1] == key) & (int)(id4[1] < e));
+        r += (int)(y[0] > key) | ((int)(y[0] == key) & (int)(id4[2] < e));
+        r += (int)(y[1] > key) | ((int)(y[1] == key) & (int)(id4[3] < e));
+      }
       if (key > none && r < K) my.best[r] = BIAS ? (double)e : key;
     }
     lds_order();

@@ -134,42 +134,45 @@ __device__ __forceinline__ int id_of(int lane, int i) {
   return ((i >> 2) * L + lane) * 4 + (i & 3);
 }
 
-// A lane's logits of token t of T; -inf where there is none (`on`: whether the token counts).  Rows of a multiple of four ids
-// are read four at a time.  Others one at a time, also where there is none (the row's last is read again): branches around
-// each would cost more.
+// The rows of the wave's tokens, t0 on, in a [T, E] array of elements of `size` bytes, as a buffer resource: what lies behind
+// the last row is read as 0 and not written.
+template <int L>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rows(const void *p, int64_t t0, int T, int E, int size) {
+  const int64_t left = T - t0;
+  const int rows = left < 0 ? 0 : left < 64 / L ? (int)left : 64 / L;
+  return __builtin_amdgcn_make_buffer_rsrc((char *)const_cast<void *>(p) + t0 * E * size, (short)0, rows * E * size, 0x00020000);
+}
+constexpr int kNowhere = 0x7ffffff0;  // an offset behind every such resource
+
+// A lane's logits of its token; -inf where there is none (`on`: whether the token counts).  t0: the wave's first token, the
+// same for all lanes.  Rows of a multiple of four ids are read four at a time, others one at a time: no branches either way.
 template <int L, int NV, bool F32>
-__device__ __forceinline__ void load_logits(const void *logits, int64_t t, int T, int E, int lane, bool on, float *l) {
+__device__ __forceinline__ void load_logits(const void *logits, int64_t t0, int T, int E, int lane, bool on, float *l) {
+  constexpr int SIZE = F32 ? 4 : 2;
+  const __amdgpu_buffer_rsrc_t rows = wave_rows<L>(logits, t0, T, E, SIZE);
+  const int off = ((int)(threadIdx.x & 63) / L * E + lane * 4) * SIZE;
   if ((E & 3) == 0) {
 #pragma unroll
     for (int c = 0; c < NV / 4; ++c) {
-      const int e = id_of<L>(lane, c * 4);
-      float *v = l + c * 4;
-      v[0] = v[1] = v[2] = v[3] = MOE_NEG_INF;
-      if (on && e < E) {
-        if constexpr (F32) {
-          const f32x4 x = *(const f32x4 *)((const float *)logits + t * E + e);
+      if constexpr (F32) {
+        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rows, off, c * L * 4 * SIZE, 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = x[k];
-        } else {
-          const u32x2 x = *(const u32x2 *)((const uint16_t *)logits + t * E + e);
+        for (int k = 0; k < 4; ++k) l[c * 4 + k] = __uint_as_float(x[k]);
+      } else {
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rows, off, c * L * 4 * SIZE, 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
-        }
+        for (int k = 0; k < 4; ++k) l[c * 4 + k] = k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
       }
     }
   } else {
-    const int64_t row = (t < T ? t : T - 1) * E;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = id_of<L>(lane, i), at = e < E ? e : E - 1;
-      float v;
-      if constexpr (F32) v = ((const float *)logits)[row + at];
-      else v = __uint_as_float((uint32_t)((const uint16_t *)logits)[row + at] << 16);
-      l[i] = on && e < E ? v : MOE_NEG_INF;
+      if constexpr (F32) l[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, off + (i & 3) * SIZE, (i >> 2) * L * 4 * SIZE, 0));
+      else l[i] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, off + (i & 3) * SIZE, (i >> 2) * L * 4 * SIZE, 0) << 16);
     }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) l[i] = usable(l[i]);
+  for (int i = 0; i < NV; ++i) l[i] = usable(on && id_of<L>(lane, i) < E ? l[i] : MOE_NEG_INF);
 }
 
 template <int L, int NV>
