@@ -1,20 +1,41 @@
 // swiglu.hip -- the gate between the two products of a layer that trains, silu(g) u with routing weights, and its
 // gradient; between the two the gate's input may be kept in 8 bits.
+#include <float.h>
+
 #include "dispatch_dev.hpp"
 #include "experts_internal.hpp"
 
 namespace moe {
 
-// The logistic function of g as a product s1 s2, and 1 - it: with t = exp(-|g| / 2), R = 1 / (1 + t t): R 1 for g >= 0, t R t
-// below, where what is multiplied between the two factors keeps its digits although exp(g) alone may be too small for fp32
-// (t is the square of exp(-|g| / 4), which is good down to |g| = 349).  1 - s is never taken as a difference.
+// The logistic function of g as a product s1 s2, and 1 - it, which is never taken as a difference.  With n = exp(-|g|) and
+// R = 1 / (1 + n) it is R for g >= 0 and n R below.  FAR: for g down to -349, where n alone may be too small for fp32 but not what
+// it multiplies: t R and t with t = exp(-|g| / 2), the square of exp(-|g| / 4), so that what stands between the two keeps its
+// digits.  Without, s2 is 1 and left out: 12 of 334 instructions a chunk of the gradient, where they count.
+template <bool FAR>
 struct Logistic {
   float s1, s2, rest;
+  __device__ __forceinline__ Logistic(float g) {
+    constexpr float kLog2e = 1.44269504088896341f;
+    if constexpr (FAR) {
+      const float q = __builtin_amdgcn_exp2f(fabsf(g) * (-0.25f * kLog2e)), t = q * q, n = t * t;
+      const float R = __builtin_amdgcn_rcpf(1.0f + n);
+      s1 = g >= 0.0f ? R : t * R;
+      s2 = g >= 0.0f ? 1.0f : t;
+      rest = g >= 0.0f ? n * R : R;
+    } else {
+      const float n = __builtin_amdgcn_exp2f(fabsf(g) * -kLog2e), R = __builtin_amdgcn_rcpf(1.0f + n), nR = n * R;
+      s1 = g >= 0.0f ? R : nR;
+      rest = g >= 0.0f ? nR : R;
+    }
+  }
+  __device__ __forceinline__ float scaled(float x) const { return FAR ? x * s2 : x; }
 };
-__device__ __forceinline__ Logistic logistic(float g) {
-  const float q = __builtin_amdgcn_exp2f(fabsf(g) * (-0.25f * 1.44269504088896341f)), t = q * q, n = t * t;
-  const float R = __builtin_amdgcn_rcpf(1.0f + n);
-  return g >= 0.0f ? Logistic{R, 1.0f, n * R} : Logistic{t * R, t, R};
+// whether a lane of the wave has a g so far out
+__device__ __forceinline__ bool far_out(const float *g) {
+  float least = g[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) least = fminf(least, g[e]);
+  return ballot(least < -80.0f) != 0;
 }
 
 __device__ __forceinline__ uint32_t pack2s(float a, float b) {
@@ -37,6 +58,16 @@ __device__ __forceinline__ float max16(float v) {
   fold(std::integral_constant<int, 0x141>{});  // row_half_mirror
   fold(std::integral_constant<int, 0x140>{});  // row_mirror
   return v;
+}
+
+// Four codes: x dyn rounded to a whole number, ties to even, by adding 1.5 2^23, whose last bits are then the code; NaN leaves 0
+// there.  No product passes 127 by half a code unless dyn is infinite (amax below 127 / FLT_MAX), which is for sat_code.
+__device__ __forceinline__ uint32_t codes4(const float *x, float dyn) {
+  if (__builtin_expect(dyn > FLT_MAX, 0)) return pack_i8x4(sat_code(x[0] * dyn), sat_code(x[1] * dyn), sat_code(x[2] * dyn), sat_code(x[3] * dyn));
+  uint32_t b[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(x[e] * dyn + 12582912.0f);
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
 }
 
 constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is left
@@ -67,11 +98,15 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
     float g[8], u[8], h[8];
     unpack8(gv, g);
     unpack8(uv, u);
+    auto gate = [&](auto far) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const Logistic s = logistic(g[e]);
-      h[e] = s.s1 * g[e] * u[e] * s.s2 * w;
-    }
+      for (int e = 0; e < 8; ++e) {
+        const Logistic<decltype(far)::value> s(g[e]);
+        h[e] = s.scaled(s.s1 * g[e] * u[e]) * w;
+      }
+    };
+    if (__builtin_expect(far_out(g), 0)) gate(std::true_type{});
+    else gate(std::false_type{});
     if (in) __builtin_nontemporal_store(pack8(h), (u32x4 *)(a.out + r * I + col));
     if constexpr (KEEP) {
       auto keep = [&](const float *x, int half) {
@@ -81,10 +116,7 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
         m = max16(m);  // by all lanes
         const float dyn = m > 0.0f ? 127.0f * (1.0f / m) : 0.0f;
         if (!in) return;
-        int c[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) c[e] = sat_code(x[e] * dyn);
-        const u32x2 v = {pack_i8x4(c[0], c[1], c[2], c[3]), pack_i8x4(c[4], c[5], c[6], c[7])};
+        const u32x2 v = {codes4(x, dyn), codes4(x + 4, dyn)};
         __builtin_nontemporal_store(v, (u32x2 *)(a.codes + r * 2 * I + half * I + col));
         if (sub == 0) a.scales[(r * 2 + half) * nb + b] = m > 0.0f ? 1.0f / dyn : 0.0f;
       };
@@ -96,8 +128,15 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
 
 // ---- backward: L threads a row, U chunks of 8 columns a thread at a time -------------------------------
 __device__ __forceinline__ void unpack_codes(u32x2 v, float scale, float *f) {
+  if (__builtin_expect(scale > 0x1p119f, 0)) {  // 128 times it may be infinite
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = (float)((int)(v[e >> 2] << (24 - 8 * (e & 3))) >> 24) * scale;
+    for (int e = 0; e < 8; ++e) f[e] = (float)((int)(v[e >> 2] << (24 - 8 * (e & 3))) >> 24) * scale;
+    return;
+  }
+  // (code + 128) scale - 128 scale: rounded once, as code scale
+  const float off = -128.0f * scale;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf((float)((v[e >> 2] ^ 0x80808080u) >> (8 * (e & 3)) & 0xffu), scale, off);
 }
 
 template <int L, int U, bool KEPT>
@@ -147,16 +186,20 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
             unpack8(gv[k], g);
             unpack8(uv[k], u);
           }
+          auto gate = [&](auto far) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const Logistic s = logistic(g[e]);
-            const float wd = w * d[e], act = s.s1 * g[e];
-            du[e] = act * wd * s.s2;
-            dg[e] = s.s1 * u[e] * wd * s.s2 * __builtin_fmaf(g[e], s.rest, 1.0f);
-            const float hu = act * u[e] * s.s2;
-            h[e] = hu * w;
-            dot = __builtin_fmaf(d[e], hu, dot);
-          }
+            for (int e = 0; e < 8; ++e) {
+              const Logistic<decltype(far)::value> s(g[e]);
+              const float wd = w * d[e], act = s.s1 * g[e];
+              du[e] = s.scaled(act * wd);
+              dg[e] = s.scaled(s.s1 * u[e] * wd) * __builtin_fmaf(g[e], s.rest, 1.0f);
+              const float hu = s.scaled(act * u[e]);
+              h[e] = hu * w;
+              dot = __builtin_fmaf(d[e], hu, dot);
+            }
+          };
+          if (__builtin_expect(far_out(g), 0)) gate(std::true_type{});
+          else gate(std::false_type{});
           if (a.gh0) {
             u32x4 *p = (u32x4 *)(a.gh0 + r * 2 * I + c * 8);
             __builtin_nontemporal_store(pack8(dg), p);

@@ -234,6 +234,27 @@ def test_blocks_that_are_zero_or_not_finite():
     assert np.array_equal(f.scales.cpu().numpy(), s)
 
 
+def test_gradient_from_the_largest_and_the_smallest_checkpoints():
+    """Blocks of bf16's largest values, whose scale times 128 leaves fp32, and of its smallest."""
+    n = 136
+    r = np.random.default_rng(13)
+    h0 = X.bf16(r, 6, 2 * n)
+    h0[0, n:] = 3.3895e38 * torch.sign(h0[0, n:])
+    h0[1, n:] *= 2.0 ** 124  # finite still
+    h0[2, n:] = 3.3895e38
+    h0[3] *= torch.tensor(2.0 ** -118).bfloat16()
+    h0[4, :n] = -3.3895e38
+    w, d = torch.ones(6), X.bf16(r, 6, n, scale=2.0 ** -20)
+    f = mg.swiglu(h0.to(X.DEV), checkpoint=True)
+    c, s, at = codes_of(h0.float().numpy())
+    assert np.array_equal(f.codes.cpu().numpy(), c) and np.array_equal(f.scales.cpu().numpy(), s)
+    g = mg.swiglu_grad(d.to(X.DEV), codes=f.codes, scales=f.scales)
+    at = at.astype(np.float64)
+    assert np.isfinite(at).all()
+    dh, eh, _, _ = backward(at, X.f64(w), X.f64(d))
+    close(g.grad_h0, dh, eh, np.ones(6, bool), "grad_h0")
+
+
 def test_rows_beyond_32_bits_of_offset():
     """Rows whose bytes begin past 2^32, in every buffer."""
     n, rows = 32768, 69000
