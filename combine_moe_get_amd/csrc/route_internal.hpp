@@ -1,5 +1,5 @@
 // route_internal.hpp -- argument blocks and launchers of the router (route.hip, balance.hip) shared with its entry
-// points (route_api.hip), and the device code that both have in common: a wave of 64 lanes holds one token's logits.
+// points (route_api.hip), and the device code that both have in common: how a token's logits lie on the lanes of a wave.
 #pragma once
 
 #include <float.h>
@@ -66,9 +66,11 @@ struct Token {
   static constexpr int LANES = L, VALUES = NV;
 };
 
-// f(Token) for T tokens of E ids.  Measured in us by lanes a token, graph replays (a launch is 2.9 of them): the choice of 8 of
-// 256 at 4096 tokens 5.0 on 16, 4.2 on 32, 4.9 on 64, at 65536 25.8, 22.2, 35.3; of 128 at 4096 tokens 4.3 on 16, 3.8 on 32,
-// at 16384 5.0, 5.9; of 512 at 4096 4.8 on 32, 5.3 on 64, at 65536 46.7, 44.7, its gradient at 4096 11.2, 10.2.
+// f(Token) for T tokens of E ids.  By lanes a token, us in graph replays (2.9 of them the launch):
+//   the choice of 8 of 256,  4096 tokens   16: 5.0   32: 4.2   64: 4.9       65536 tokens   16: 25.8   32: 22.2   64: 35.3
+//   the choice of 8 of 128,  4096 tokens   16: 4.3   32: 3.8                 16384 tokens   16: 5.0    32: 5.9
+//   the choice of 8 of 512,  4096 tokens             32: 4.8   64: 5.3       65536 tokens              32: 46.7   64: 44.7
+//   the gradient of 512,     4096 tokens             32: 11.2  64: 10.2
 template <class F>
 inline void with_token(int T, int E, F &&f) {
   if (E <= 64) f(Token<16, 4>{});
@@ -135,7 +137,8 @@ __device__ __forceinline__ int id_of(int lane, int i) {
 }
 
 // The rows of the wave's tokens, t0 on, in a [T, E] array of elements of `size` bytes, as a buffer resource: what lies behind
-// the last row is read as 0 and not written.
+// the last row is read as 0 and not written.  The check is of the vector offset with the instruction's, not of a scalar one,
+// which stays 0.
 template <int L>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rows(const void *p, int64_t t0, int T, int E, int size) {
   const int64_t left = T - t0;
@@ -155,11 +158,11 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t t0, int 
 #pragma unroll
     for (int c = 0; c < NV / 4; ++c) {
       if constexpr (F32) {
-        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rows, off, c * L * 4 * SIZE, 0);
+        const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(rows, off + c * L * 4 * SIZE, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) l[c * 4 + k] = __uint_as_float(x[k]);
       } else {
-        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rows, off, c * L * 4 * SIZE, 0);
+        const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(rows, off + c * L * 4 * SIZE, 0, 0);
 #pragma unroll
         for (int k = 0; k < 4; ++k) l[c * 4 + k] = k & 1 ? bf16_hi(x[k >> 1]) : bf16_lo(x[k >> 1]);
       }
@@ -167,8 +170,9 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t t0, int 
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (F32) l[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, off + (i & 3) * SIZE, (i >> 2) * L * 4 * SIZE, 0));
-      else l[i] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, off + (i & 3) * SIZE, (i >> 2) * L * 4 * SIZE, 0) << 16);
+      const int at = off + ((i >> 2) * L * 4 + (i & 3)) * SIZE;
+      if constexpr (F32) l[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, at, 0, 0));
+      else l[i] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rows, at, 0, 0) << 16);
     }
   }
 #pragma unroll

@@ -10,7 +10,7 @@ namespace moe {
 // The logistic function of g as a product s1 s2, and 1 - it, which is never taken as a difference.  With n = exp(-|g|) and
 // R = 1 / (1 + n) it is R for g >= 0 and n R below.  FAR: for g down to -349, where n alone may be too small for fp32 but not what
 // it multiplies: t R and t with t = exp(-|g| / 2), the square of exp(-|g| / 4), so that what stands between the two keeps its
-// digits.  Without, s2 is 1 and left out: 12 of 334 instructions a chunk of the gradient, where they count.
+// digits.  Without, s2 is 1 and left out (32768 rows of 2 x 2048: forward 99 -> 95 us, gradient 114 -> 110).
 template <bool FAR>
 struct Logistic {
   float s1, s2, rest;
@@ -74,9 +74,10 @@ constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is lef
 
 // ---- forward: 16 lanes a block of 128 columns of a row, 8 of each half a lane -----------------------
 //
-// One pass, bound by memory: 32768 rows of 2 x 2048 105 us with codes (541 MB, 5.2 TB/s; a large copy reaches 5.1), 68
-// without (403 MB, 5.9 TB/s).  Stores go past the caches (106 and 85 us where they do not: the lines they would leave there
-// are the next reader's only where rows are few).  Two blocks a thread take 108, four more registers than it pays.
+// One pass, bound by memory: 32768 rows of 2 x 2048 with codes 94 us (541 MB, 5.7 TB/s; a large copy reaches 5.1), without 68
+// (403 MB, 5.9 TB/s).  A thread's 16 values take some 320 instructions, which nearly fill that time: with codes rounded, clamped
+// and packed by the book it was them that bound it (108 us).  Stores go past the caches: 116 and 85 us where they do not, the
+// gradient 159 for 155.  Two blocks a thread take 107 us, and 4.8 for 3.8 on 400 rows of 2 x 512.
 template <bool KEEP>
 __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
   const int sub = threadIdx.x & 15, I = a.I;
@@ -127,6 +128,9 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
 }
 
 // ---- backward: L threads a row, U chunks of 8 columns a thread at a time -------------------------------
+//
+// One pass as well: the row's sum for its weight's gradient is folded over the L threads.  32768 rows of 2048 from codes 110 us
+// (675 MB, 6.1 TB/s), 8192 of 4096 from bf16 70 us (403 MB, 5.8 TB/s).
 __device__ __forceinline__ void unpack_codes(u32x2 v, float scale, float *f) {
   if (__builtin_expect(scale > 0x1p119f, 0)) {  // 128 times it may be infinite
 #pragma unroll
@@ -245,13 +249,13 @@ static void launch_grad(const SwigluArgs &a, hipStream_t st) {
 // Threads a row: as many as keep each busy, with two chunks from codes (which are half as wide: a wave has too little under
 // way with one), with one from bf16.  us, from codes / from bf16, by threads a row:
 //                          16           32           64          128          256
-//   65536 rows of  256   36 / 38      47 / 42      81 / 55     126 / 87     218 / 155
-//   32768 rows of  512   36 / 39      35 / 38      47 / 37      72 / 50     118 / 85
-//   30000 rows of 1024   61 / 72      57 / 66      59 / 64      82 / 63     127 / 91
-//   32768 rows of 2048  161 / 202    132 / 163    118 / 148    122 / 135    173 / 132
-//    6168 rows of 2056   55 / 63      46 / 52      34 / 40      32 / 34      41 / 33
-//    8192 rows of 4096   77 / 95      73 / 84      66 / 76      63 / 75      64 / 70
-//     100 rows of 8192   42 / 56      25 / 30      14 / 16     8.8 / 9.7    6.2 / 6.7
+//   65536 rows of  256   34 / 37      43 / 37      70 / 48     104 / 74     177 / 126
+//   32768 rows of  512   34 / 41      34 / 38      41 / 37      61 / 44      98 / 71
+//   30000 rows of 1024   61 / 72      56 / 67      55 / 64      72 / 63     108 / 78
+//   32768 rows of 2048  145 / 189    130 / 158    117 / 145    111 / 140    147 / 132
+//    6168 rows of 2056   52 / 62      42 / 51      32 / 39      29 / 34      34 / 32
+//    8192 rows of 4096   79 / 95      67 / 83      65 / 76      62 / 74      58 / 72
+//     100 rows of 8192   42 / 53      25 / 28      14 / 15     8.9 / 9.6    6.2 / 6.7
 hipError_t launch_swiglu_grad(const SwigluArgs &a, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
   const int chunks = a.I / (a.codes ? 16 : 8);

