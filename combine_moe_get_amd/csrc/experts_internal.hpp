@@ -88,6 +88,8 @@ struct SwigluArgs {
   float *gw;
   int64_t rows;
   int32_t I;
+  uint32_t div_nb;       // set by the launcher: blocks of 128 columns of a half as a divisor
+  double over_nb;
 };
 hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t stream);
 hipError_t launch_swiglu_grad(const SwigluArgs &a, hipStream_t stream);

@@ -60,14 +60,24 @@ __device__ __forceinline__ float max16(float v) {
   return v;
 }
 
+// 1 / x for x between 2^-100 and 2^100 whose mantissa is a bf16's, or 127 times the reciprocal of one: one Newton step from the
+// instruction's value, exact but for its last rounding, which leaves less than 2^-44; none of the 256 mantissas has its
+// reciprocal that near to the middle between two fp32 values.
+__device__ __forceinline__ float reciprocal(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return __builtin_fmaf(__builtin_fmaf(-x, r, 1.0f), r, r);
+}
+
 // Four codes: x dyn rounded to a whole number, ties to even, by adding 1.5 2^23, whose last bits are then the code; NaN leaves 0
-// there.  No product passes 127 by half a code unless dyn is infinite (amax below 127 / FLT_MAX), which is for sat_code.
+// there.  No product passes 127 by half a code while dyn is finite.
 __device__ __forceinline__ uint32_t codes4(const float *x, float dyn) {
-  if (__builtin_expect(dyn > FLT_MAX, 0)) return pack_i8x4(sat_code(x[0] * dyn), sat_code(x[1] * dyn), sat_code(x[2] * dyn), sat_code(x[3] * dyn));
   uint32_t b[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(x[e] * dyn + 12582912.0f);
   return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u), __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
+}
+__device__ __forceinline__ uint32_t codes4_any(const float *x, float dyn) {
+  return pack_i8x4(sat_code(x[0] * dyn), sat_code(x[1] * dyn), sat_code(x[2] * dyn), sat_code(x[3] * dyn));
 }
 
 constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is left
@@ -80,21 +90,24 @@ constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is lef
 // gradient 159 for 155.  Two blocks a thread take 107 us, and 4.8 for 3.8 on 400 rows of 2 x 512.
 template <bool KEEP>
 __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
-  const int sub = threadIdx.x & 15, I = a.I;
-  const uint32_t nb = (uint32_t)(I + 127) / 128;
+  const int sub = threadIdx.x & 15;
+  const uint32_t I = a.I, nb = (I + 127) / 128;
   for (uint64_t first = (uint64_t)blockIdx.x * 16; first < (uint64_t)a.rows * nb; first += (uint64_t)gridDim.x * 16) {
-    const uint64_t row0 = first / nb;  // the workgroup's 16 blocks, in the order of rows
-    const uint32_t i = (uint32_t)(first - row0 * nb) + (threadIdx.x >> 4), q = i / nb, b = i - q * nb;
-    const int64_t r = (int64_t)row0 + q;
-    const int col = (int)b * 128 + sub * 8;
-    const bool in = r < a.rows && row_used(a.g, r) && col < I;
+    // the workgroup's 16 blocks, in the order of rows: from this row on (floor(first / nb): half a block from the next whole number)
+    const int64_t at = (int64_t)(((double)first + 0.5) * a.over_nb);
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(at >> 32)) << 32 | (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+    const uint32_t i = (uint32_t)(first - (uint64_t)row0 * nb) + (threadIdx.x >> 4), q = fast_div((int)i, a.div_nb), b = i - q * nb;
+    const uint32_t col = b * 128 + sub * 8;
+    const bool in = row0 + q < a.rows && col < I && row_used(a.g, row0 + q);
+    // within the workgroup's rows 32 bits of offset do: at most 16 rows of one block, or two and some of more
+    const uint32_t two = q * 2 * I + col, one = q * I + col;
     u32x4 gv = {0u, 0u, 0u, 0u}, uv = gv;
     float w = 1.0f;
     if (in) {
-      const uint16_t *p = a.h0 + r * 2 * I + col;
-      gv = *(const u32x4 *)p;
-      uv = *(const u32x4 *)(p + I);
-      if (a.w) w = a.w[r];
+      const uint16_t *p = a.h0 + row0 * 2 * I;
+      gv = *(const u32x4 *)(p + two);
+      uv = *(const u32x4 *)(p + two + I);
+      if (a.w) w = a.w[row0 + q];
     }
     float g[8], u[8], h[8];
     unpack8(gv, g);
@@ -108,21 +121,42 @@ __global__ void __launch_bounds__(256) swiglu_kernel(SwigluArgs a) {
     };
     if (__builtin_expect(far_out(g), 0)) gate(std::true_type{});
     else gate(std::false_type{});
-    if (in) __builtin_nontemporal_store(pack8(h), (u32x4 *)(a.out + r * I + col));
+    if (in) __builtin_nontemporal_store(pack8(h), (u32x4 *)(a.out + row0 * I + one));
     if constexpr (KEEP) {
-      auto keep = [&](const float *x, int half) {
+      auto largest = [&](const float *x) {
         float m = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-        m = max16(m);  // by all lanes
-        const float dyn = m > 0.0f ? 127.0f * (1.0f / m) : 0.0f;
-        if (!in) return;
-        const u32x2 v = {codes4(x, dyn), codes4(x + 4, dyn)};
-        __builtin_nontemporal_store(v, (u32x2 *)(a.codes + r * 2 * I + half * I + col));
-        if (sub == 0) a.scales[(r * 2 + half) * nb + b] = m > 0.0f ? 1.0f / dyn : 0.0f;
+        return max16(m);
       };
-      keep(g, 0);
-      keep(u, 1);
+      const float mg = largest(g), mu = largest(u);
+      float dg, du, sg, su;
+      u32x2 cg, cu;
+      if (__builtin_expect(ballot(!(fminf(mg, mu) > 0x1p-100f && fmaxf(mg, mu) < 0x1p100f)) == 0, 1)) {
+        dg = 127.0f * reciprocal(mg);
+        du = 127.0f * reciprocal(mu);
+        sg = reciprocal(dg);
+        su = reciprocal(du);
+        cg = u32x2{codes4(g, dg), codes4(g + 4, dg)};
+        cu = u32x2{codes4(u, du), codes4(u + 4, du)};
+      } else {  // a block of zeros, or of values so small or large that reciprocals leave the normal numbers
+        dg = mg > 0.0f ? 127.0f * (1.0f / mg) : 0.0f;
+        du = mu > 0.0f ? 127.0f * (1.0f / mu) : 0.0f;
+        sg = mg > 0.0f ? 1.0f / dg : 0.0f;
+        su = mu > 0.0f ? 1.0f / du : 0.0f;
+        cg = u32x2{codes4_any(g, dg), codes4_any(g + 4, dg)};
+        cu = u32x2{codes4_any(u, du), codes4_any(u + 4, du)};
+      }
+      if (in) {
+        int8_t *c = a.codes + row0 * 2 * I;
+        __builtin_nontemporal_store(cg, (u32x2 *)(c + two));
+        __builtin_nontemporal_store(cu, (u32x2 *)(c + two + I));
+        float *s = a.scales + row0 * 2 * nb;
+        if (sub == 0) {
+          s[q * 2 * nb + b] = sg;
+          s[q * 2 * nb + nb + b] = su;
+        }
+      }
     }
   }
 }
@@ -229,9 +263,13 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
   }
 }
 
-hipError_t launch_swiglu(const SwigluArgs &a, hipStream_t st) {
+hipError_t launch_swiglu(const SwigluArgs &a_, hipStream_t st) {
+  SwigluArgs a = a_;
   if (a.rows == 0) return hipSuccess;
-  const uint64_t wg = ((uint64_t)a.rows * ((a.I + 127) / 128) + 15) / 16;
+  const int nb = (a.I + 127) / 128;
+  a.over_nb = 1.0 / nb;
+  a.div_nb = div_magic(nb);  // of numbers below nb + 16
+  const uint64_t wg = ((uint64_t)a.rows * nb + 15) / 16;
   const dim3 grid((unsigned)(wg < kMostGroups ? wg : kMostGroups)), block(256);
   if (a.codes) hipLaunchKernelGGL((swiglu_kernel<true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((swiglu_kernel<false>), grid, block, 0, st, a);

@@ -234,6 +234,22 @@ def test_blocks_that_are_zero_or_not_finite():
     assert np.array_equal(f.scales.cpu().numpy(), s)
 
 
+def test_every_amax():
+    """Blocks with every finite bf16 as their largest: dyn and scale are two roundings of it, the codes one more."""
+    top = torch.from_numpy(np.arange(1, 0x7f80, dtype=np.int16)).view(torch.bfloat16)
+    top = torch.cat((top, top[-1:]))  # an even number: two halves a row
+    r = np.random.default_rng(17)
+    x = torch.from_numpy(r.uniform(-1, 1, (len(top), 128)).astype(np.float32)) * top.float()[:, None]
+    x = x.bfloat16()
+    x[:, 7] = top
+    x[:, 50] = -top / 2  # half of it, exactly
+    h0 = x.view(-1, 256)
+    f = mg.swiglu(h0.to(X.DEV), checkpoint=True)
+    c, s, _ = codes_of(h0.float().numpy())
+    assert np.array_equal(f.scales.cpu().numpy(), s)
+    assert np.array_equal(f.codes.cpu().numpy(), c)
+
+
 def test_gradient_from_the_largest_and_the_smallest_checkpoints():
     """Blocks of bf16's largest values, whose scale times 128 leaves fp32, and of its smallest."""
     n = 136
