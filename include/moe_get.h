@@ -469,7 +469,7 @@ int moe_route_check_shape(const moe_route_shape_t *shape);
  * 32 would let their rounding choose; keys within some 1e-15 of one another may come in either order); otherwise the
  * logits, which have the same order.  The topk_groups best groups; of their ids the K best, in descending order.  Ties go
  * to the lowest group or id.  The bias chooses only:
- *   topk_weights[t, j] = scale * s[t, e_j]          (renormalize: s[t, e_j] / sum_i s[t, e_i], exact where both underflow)
+ *   topk_weights[t, j] = scale * s[t, e_j]          (renormalize: s[t, e_j] / sum_i s[t, e_i], also where all of them vanish in fp32)
  * Slots for which no id is left hold -1 (which the layout drops) and weight 0; so do all slots of tokens that are not live.
  *  logits_fp32        1: logits are float32, 0: bf16
  *  in  logits [T, E], 16-byte aligned
