@@ -47,16 +47,17 @@ __device__ __forceinline__ void group_best(const RouteArgs &a, int lane, V none,
       V one = none, two = none;
 #pragma unroll
       for (int k = 0; k < 4; ++k) best_two(one, two, value(c * 4 + k), none);
-      auto step = [&](auto ctrl) {
-        constexpr int CTRL = decltype(ctrl)::value;
-        const V other = dpp<CTRL>(one);
-        if (a.two) best_two(one, two, other, dpp<CTRL>(two));
+      auto step = [&](auto move) {
+        const V other = move(one);
+        if (a.two) best_two(one, two, other, move(two));
         else one = one > other ? one : other;
       };
-      if (a.span > 1) step(std::integral_constant<int, 0xb1>{});
-      if (a.span > 2) step(std::integral_constant<int, 0x4e>{});
-      if (a.span > 4) step(std::integral_constant<int, 0x141>{});
-      if (a.span > 8) step(std::integral_constant<int, 0x140>{});
+      if (a.span > 1) step([](V x) { return dpp<0xb1>(x); });
+      if (a.span > 2) step([](V x) { return dpp<0x4e>(x); });
+      if (a.span > 4) step([](V x) { return dpp<0x141>(x); });
+      if (a.span > 8) step([](V x) { return dpp<0x140>(x); });
+      if (L > 16 && a.span > 16) step([](V x) { return __shfl_xor(x, 16); });
+      if (L > 32 && a.span > 32) step([](V x) { return __shfl_xor(x, 32); });
       const int at = c * L + lane, g = at >> a.span_log;
       if ((at & (a.span - 1)) == 0 && g < a.G) put(one, two, g);
     }
@@ -359,8 +360,12 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
 }
 
 template <int L, int NV>
-static void launch_sized(const RouteArgs &a, int score, bool fp32, hipStream_t st) {
+static void launch_sized(const RouteArgs &a_, int score, bool fp32, hipStream_t st) {
   constexpr int TOKENS = 4 * (64 / L);  // a workgroup
+  RouteArgs a = a_;
+  const int per = a.E / a.G, quads = per / 4;
+  a.span = per % 4 == 0 && (quads & (quads - 1)) == 0 && quads <= L ? quads : 0;
+  a.span_log = a.span ? __builtin_ctz(a.span) : 0;
   const dim3 grid((unsigned)((a.T + TOKENS - 1) / TOKENS)), block(256);
   auto go = [&](auto sc, auto f32, auto bias) {
     hipLaunchKernelGGL((route_kernel<L, NV, decltype(sc)::value, decltype(f32)::value, decltype(bias)::value>), grid, block, 0,
@@ -379,10 +384,7 @@ static void launch_sized(const RouteArgs &a, int score, bool fp32, hipStream_t s
 hipError_t launch_route(const RouteArgs &a_, int score, bool fp32, hipStream_t st) {
   RouteArgs a = a_;
   if (a.T == 0) return hipSuccess;
-  const int per = a.E / a.G, quads = per / 4;
-  a.div_per = div_magic(per);
-  a.span = per % 4 == 0 && (quads & (quads - 1)) == 0 && quads <= 16 ? quads : 0;
-  a.span_log = a.span ? __builtin_ctz(a.span) : 0;
+  a.div_per = div_magic(a.E / a.G);
   with_token(a.T, a.E, [&](auto tok) { launch_sized<decltype(tok)::LANES, decltype(tok)::VALUES>(a, score, fp32, st); });
   return hipGetLastError();
 }

@@ -17,8 +17,8 @@ struct RouteArgs {
   int32_t T, E, K, G, keep;
   int32_t two, renorm;
   float scale;
-  // set by the launcher: div_magic of the ids of a group; lanes that hold four each of them, if these are a power of two up
-  // to 16 (else 0), and its logarithm
+  // set by the launcher: div_magic of the ids of a group; lanes that hold four each of them, if these are a power of two and
+  // no more than a token has (else 0), and its logarithm
   uint32_t div_per;
   int32_t span, span_log;
 };
