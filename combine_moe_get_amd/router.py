@@ -85,15 +85,22 @@ def balance_workspace_size(shape, balance):
     return _lib().moe_balance_workspace_size(ctypes.byref(shape), ctypes.byref(balance))
 
 
+_FP32 = {torch.float32: 1, torch.bfloat16: 0}  # what logits may be
+
+
 def _logits(shape, logits, what):
-    """Device and type flag of the logits of a call with a valid shape."""
+    """Device, type flag and address of the logits of a call, whose shape is valid."""
     dev = _device_of(logits, "logits")
-    st = check_route_shape(shape)
+    st = _lib().moe_route_check_shape(ctypes.byref(shape))
     if st != B.MOE_OK:
         raise B.MoeGetError(what, st)
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    fp32 = _FP32.get(logits.dtype)
+    if fp32 is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    return dev, int(logits.dtype == torch.float32)
+    numel = shape.num_tokens * shape.num_ids
+    if not logits.is_contiguous() or logits.numel() < numel:
+        B._ptr(logits, "logits", (logits.dtype,), numel)  # says what is wrong
+    return dev, fp32, logits.data_ptr() or None
 
 
 Route = namedtuple("Route", ["topk_idx", "topk_weights"])
@@ -101,15 +108,15 @@ Route = namedtuple("Route", ["topk_idx", "topk_weights"])
 
 def prepare_route(shape, logits, bias=None, x_active_mask=None, topk_idx=None, topk_weights=None):
     """Checked, marshalled moe_route call; see route()."""
-    dev, fp32 = _logits(shape, logits, "route")
+    dev, fp32, logits_p = _logits(shape, logits, "route")
     T, E, K = shape.num_tokens, shape.num_ids, shape.topk
     topk_idx, idx_p = _result(topk_idx, "topk_idx", torch.int32, (T, K), (K, 1), dev)
     topk_weights, w_p = _result(topk_weights, "topk_weights", torch.float32, (T, K), (K, 1), dev)
     args = [
         ctypes.byref(shape), fp32,
-        _ptr(logits, "logits", (logits.dtype,), T * E, dev),
-        _ptr(bias, "bias", B.F32, E, dev, required=False),
-        _ptr(x_active_mask, "x_active_mask", B.U8, T, dev, required=False),
+        logits_p,
+        None if bias is None else _ptr(bias, "bias", B.F32, E, dev),
+        None if x_active_mask is None else _ptr(x_active_mask, "x_active_mask", B.U8, T, dev),
         idx_p, w_p, None,
     ]
     return ExpertsCall(_lib().moe_route, args, "route", (shape, logits, bias, x_active_mask),
@@ -129,7 +136,7 @@ BalanceLoss = namedtuple("BalanceLoss", ["losses", "counts", "prob_sums", "segme
 
 def prepare_balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, workspace=None):
     """Checked, marshalled moe_balance_loss call; see balance_loss()."""
-    dev, fp32 = _logits(shape, logits, "balance_loss")
+    dev, fp32, logits_p = _logits(shape, logits, "balance_loss")
     T, E, K, S = shape.num_tokens, shape.num_ids, shape.topk, balance.segments
     need = balance_workspace_size(shape, balance)
     if need == 0:
@@ -141,9 +148,9 @@ def prepare_balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, w
     tokens, tokens_p = _result(None, "segment_tokens", torch.int32, (S,), (1,), dev)
     args = [
         ctypes.byref(shape), ctypes.byref(balance), fp32,
-        _ptr(logits, "logits", (logits.dtype,), T * E, dev),
+        logits_p,
         _ptr(topk_idx, "topk_idx", B.I32, T * K, dev),
-        _ptr(x_active_mask, "x_active_mask", B.U8, T, dev, required=False),
+        None if x_active_mask is None else _ptr(x_active_mask, "x_active_mask", B.U8, T, dev),
         losses_p, counts_p, sums_p, tokens_p, ws_p, workspace.numel(), None,
     ]
     return ExpertsCall(_lib().moe_balance_loss, args, "balance_loss",
@@ -164,7 +171,7 @@ def balance_loss(shape, balance, logits, topk_idx, x_active_mask=None, workspace
 def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=None, balance_loss=None, grad_losses=None,
                        x_active_mask=None, dst_row=None, out=None):
     """Checked, marshalled moe_route_grad call; see route_grad()."""
-    dev, fp32 = _logits(shape, logits, "route_grad")
+    dev, fp32, logits_p = _logits(shape, logits, "route_grad")
     T, E, K = shape.num_tokens, shape.num_ids, shape.topk
     if (balance is None) != (balance_loss is None):
         raise ValueError("balance and balance_loss go together")
@@ -180,11 +187,11 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
     out, out_p = _result(out, "out", logits.dtype, (T, E), (E, 1), dev)
     args = [
         ctypes.byref(shape), fp32,
-        _ptr(logits, "logits", (logits.dtype,), T * E, dev),
+        logits_p,
         _ptr(topk_idx, "topk_idx", B.I32, T * K, dev, required=grad_topk_weights is not None),
         _ptr(grad_topk_weights, "grad_topk_weights", B.F32, T * K if dst_row is None else None, dev, required=False),
-        _ptr(dst_row, "dst_row", B.I32, T * K, dev, required=False),
-        _ptr(x_active_mask, "x_active_mask", B.U8, T, dev, required=False),
+        None if dst_row is None else _ptr(dst_row, "dst_row", B.I32, T * K, dev),
+        None if x_active_mask is None else _ptr(x_active_mask, "x_active_mask", B.U8, T, dev),
         ctypes.byref(balance) if balance is not None else None,
         _ptr(counts, "counts", B.I32, S * E, dev, required=False),
         _ptr(tokens, "segment_tokens", B.I32, S, dev, required=False),
