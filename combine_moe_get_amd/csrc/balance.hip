@@ -398,11 +398,17 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
       // of the logarithms of the scores of the token's ids: slot j on lane j
       float aj, sum_a = 0.0f, s, s_rest;
       if (a.renorm) {
-        scores<1, SCORE>(&lj, max_of<L>(lj), &s, &s_rest);
+        // divided, as in the choice, and about the gradient of a slot with the largest score: one that carries the sum loses no
+        // digits of the others', and where one slot alone has a score the result is 0 exactly
+        const float top = max_of<L>(lj);
+        scores<1, SCORE>(&lj, top, &s, &s_rest);
         const float all = sum_of<L>(some ? s : 0.0f);
-        const float w = some ? s * __builtin_amdgcn_rcpf(all) : 0.0f;
-        const float mean = sum_of<L>(w * gw);
-        aj = a.scale * w * (gw - mean);
+        const float w = some ? s / all : 0.0f;
+        const uint64_t best = token_bits<L>(ballot(some && lj == top));
+        const float g0 = __shfl(gw, best ? __builtin_ctzll(best) : 0, L);
+        const float diff = some ? gw - g0 : 0.0f;
+        const float mean = sum_of<L>(w * diff);
+        aj = some ? a.scale * w * (diff - mean) : 0.0f;
       } else {
         s = SCORE == MOE_SCORE_SOFTMAX ? exp_neg(lj - m) * r : sigmoid(lj, s_rest);
         aj = some ? a.scale * s * gw : 0.0f;

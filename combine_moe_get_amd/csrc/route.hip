@@ -77,12 +77,6 @@ __device__ __forceinline__ void group_best(const RouteArgs &a, int lane, V none,
   }
 }
 
-// bits of a token's lanes in a ballot
-template <int L>
-__device__ __forceinline__ uint64_t token_bits(uint64_t m) {
-  return L == 64 ? m : (m >> (threadIdx.x & 63 & ~(L - 1))) & ((1ull << (L & 63)) - 1);
-}
-
 // LDS of a token: up to 4 L candidates (before them the groups' scores), its K results
 template <int L>
 struct RouteLds {

@@ -120,6 +120,12 @@ __device__ __forceinline__ V sum_of(V v) {
   return fold<L>(v, [](V a, V b) { return a + b; });
 }
 
+// bits of a token's lanes in a ballot
+template <int L>
+__device__ __forceinline__ uint64_t token_bits(uint64_t m) {
+  return L == 64 ? m : (m >> (threadIdx.x & 63 & ~(L - 1))) & ((1ull << (L & 63)) - 1);
+}
+
 // LDS accesses of a wave are in order; this keeps the compiler to it
 __device__ __forceinline__ void lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
