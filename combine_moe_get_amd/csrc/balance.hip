@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256) route_grad_kernel(RouteGradArgs a) {
         gw = a.gw[at];
       } else {
         const int r = a.dst[at];
-        if (r >= 0) gw = a.gw[r];
+        if (r >= 0 && r < a.rows) gw = a.gw[r];
       }
     }
     const bool some = lj > MOE_NEG_INF;

@@ -32,6 +32,45 @@ int check_balance(const moe_route_shape_t *s, const moe_balance_t *b) {
 
 int done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
+// rows: those of grad_weights where there is a dst_row
+int route_grad(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
+               const float *grad_weights, int32_t rows, const int32_t *dst_row, const uint8_t *x_active_mask,
+               const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
+               const float *grad_losses, void *grad_logits, void *stream) {
+  int st = check_shape(shape);
+  if (st == MOE_OK && balance) st = check_balance(shape, balance);
+  if (st != MOE_OK) return st;
+  if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_ARG;
+  if (!balance && (counts || segment_tokens || grad_losses)) return MOE_ERR_ARG;
+  if (shape->num_tokens == 0) return MOE_OK;
+  if ((!balance || dst_row) && !grad_weights) return MOE_ERR_ARG;
+  if (!logits || !grad_logits || !aligned(logits, 16) || !aligned(grad_logits, 16)) return MOE_ERR_ARG;
+  if (grad_weights && (!topk_idx || !aligned(topk_idx, 4) || !aligned(grad_weights, 4) || !aligned(dst_row, 4)))
+    return MOE_ERR_ARG;
+  if (balance && (!counts || !segment_tokens || !aligned(counts, 4) || !aligned(segment_tokens, 4) || !aligned(grad_losses, 4)))
+    return MOE_ERR_ARG;
+  RouteGradArgs a;
+  a.logits = logits;
+  a.idx = topk_idx;
+  a.gw = grad_weights;
+  a.dst = dst_row;
+  a.mask = x_active_mask;
+  a.counts = counts;
+  a.tokens = segment_tokens;
+  a.gl = grad_losses;
+  a.out = grad_logits;
+  a.T = shape->num_tokens;
+  a.E = shape->num_ids;
+  a.K = shape->topk;
+  a.S = balance ? balance->segments : 1;
+  a.renorm = shape->renormalize;
+  a.rows = rows;
+  a.scale = shape->scale;
+  a.balance_coef = balance ? balance->balance_coef : 0.0f;
+  a.z_coef = balance ? balance->z_coef : 0.0f;
+  return done(launch_route_grad(a, shape->score, logits_fp32 != 0, (hipStream_t)stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -104,37 +143,22 @@ int moe_route_grad(const moe_route_shape_t *shape, int32_t logits_fp32, const vo
                    const float *grad_topk_weights, const int32_t *dst_row, const uint8_t *x_active_mask,
                    const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
                    const float *grad_losses, void *grad_logits, void *stream) {
-  int st = check_shape(shape);
-  if (st == MOE_OK && balance) st = check_balance(shape, balance);
+  return route_grad(shape, logits_fp32, logits, topk_idx, grad_topk_weights, INT32_MAX, dst_row, x_active_mask, balance, counts,
+                    segment_tokens, grad_losses, grad_logits, stream);
+}
+
+int moe_route_grad_rows(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
+                        const float *grad_row_weights, int64_t rows, const int32_t *dst_row, const uint8_t *x_active_mask,
+                        const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
+                        const float *grad_losses, void *grad_logits, void *stream) {
+  const int st = check_shape(shape);
   if (st != MOE_OK) return st;
-  if (logits_fp32 != 0 && logits_fp32 != 1) return MOE_ERR_ARG;
-  if (!balance && (counts || segment_tokens || grad_losses)) return MOE_ERR_ARG;
-  if (shape->num_tokens == 0) return MOE_OK;
-  if ((!balance || dst_row) && !grad_topk_weights) return MOE_ERR_ARG;
-  if (!logits || !grad_logits || !aligned(logits, 16) || !aligned(grad_logits, 16)) return MOE_ERR_ARG;
-  if (grad_topk_weights && (!topk_idx || !aligned(topk_idx, 4) || !aligned(grad_topk_weights, 4) || !aligned(dst_row, 4)))
-    return MOE_ERR_ARG;
-  if (balance && (!counts || !segment_tokens || !aligned(counts, 4) || !aligned(segment_tokens, 4) || !aligned(grad_losses, 4)))
-    return MOE_ERR_ARG;
-  RouteGradArgs a;
-  a.logits = logits;
-  a.idx = topk_idx;
-  a.gw = grad_topk_weights;
-  a.dst = dst_row;
-  a.mask = x_active_mask;
-  a.counts = counts;
-  a.tokens = segment_tokens;
-  a.gl = grad_losses;
-  a.out = grad_logits;
-  a.T = shape->num_tokens;
-  a.E = shape->num_ids;
-  a.K = shape->topk;
-  a.S = balance ? balance->segments : 1;
-  a.renorm = shape->renormalize;
-  a.scale = shape->scale;
-  a.balance_coef = balance ? balance->balance_coef : 0.0f;
-  a.z_coef = balance ? balance->z_coef : 0.0f;
-  return done(launch_route_grad(a, shape->score, logits_fp32 != 0, (hipStream_t)stream));
+  if (rows < 0) return MOE_ERR_SHAPE;
+  if (shape->num_tokens > 0 && (!dst_row || (rows > 0 && !grad_row_weights))) return MOE_ERR_ARG;
+  // without rows there is nothing to read, and the slots' gradients are zeros
+  const float *g = rows > 0 ? grad_row_weights : (const float *)dst_row;
+  return route_grad(shape, logits_fp32, logits, topk_idx, g, rows < INT32_MAX ? (int32_t)rows : INT32_MAX, dst_row,
+                    x_active_mask, balance, counts, segment_tokens, grad_losses, grad_logits, stream);
 }
 
 }  // extern "C"

@@ -43,13 +43,13 @@ struct RouteGradArgs {
   const void *logits;
   const int32_t *idx;
   const float *gw;
-  const int32_t *dst;              // null: gw is [T, K]; else it is of receive rows, and this their map
+  const int32_t *dst;              // null: gw is [T, K]; else it is of `rows` receive rows, and this their map
   const uint8_t *mask;
   const int32_t *counts, *tokens;  // null: no losses
   const float *gl;
   void *out;
   int32_t T, E, K, S;
-  int32_t renorm;
+  int32_t renorm, rows;
   float scale, balance_coef, z_coef;
 };
 hipError_t launch_route_grad(const RouteGradArgs &a, int score, bool fp32, hipStream_t stream);

@@ -61,14 +61,15 @@ def _lib():
     global _fns
     if _fns is None:
         L = B.lib()
-        V, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        V, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         SP, BP = ctypes.POINTER(RouteShape), ctypes.POINTER(Balance)
         for name, args, res in (
                 ("moe_route_check_shape", [SP], ctypes.c_int),
                 ("moe_route", [SP, I32] + [V] * 6, ctypes.c_int),
                 ("moe_balance_workspace_size", [SP, BP], SZ),
                 ("moe_balance_loss", [SP, BP, I32] + [V] * 8 + [SZ, V], ctypes.c_int),
-                ("moe_route_grad", [SP, I32] + [V] * 5 + [BP] + [V] * 5, ctypes.c_int)):
+                ("moe_route_grad", [SP, I32] + [V] * 5 + [BP] + [V] * 5, ctypes.c_int),
+                ("moe_route_grad_rows", [SP, I32] + [V] * 3 + [I64] + [V] * 2 + [BP] + [V] * 5, ctypes.c_int)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         _fns = L
@@ -190,6 +191,7 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
         logits_p,
         _ptr(topk_idx, "topk_idx", B.I32, T * K, dev, required=grad_topk_weights is not None),
         _ptr(grad_topk_weights, "grad_topk_weights", B.F32, T * K if dst_row is None else None, dev, required=False),
+        *(() if dst_row is None else (grad_topk_weights.numel(),)),
         None if dst_row is None else _ptr(dst_row, "dst_row", B.I32, T * K, dev),
         None if x_active_mask is None else _ptr(x_active_mask, "x_active_mask", B.U8, T, dev),
         ctypes.byref(balance) if balance is not None else None,
@@ -198,7 +200,7 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
         _ptr(grad_losses, "grad_losses", B.F32, 2, dev, required=False),
         out_p, None,
     ]
-    return ExpertsCall(_lib().moe_route_grad, args, "route_grad",
+    return ExpertsCall(_lib().moe_route_grad if dst_row is None else _lib().moe_route_grad_rows, args, "route_grad",
                        (shape, logits, topk_idx, grad_topk_weights, dst_row, x_active_mask, balance, counts, tokens, grad_losses),
                        out, dev)
 
@@ -211,6 +213,6 @@ def route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=None, ba
       balance, balance_loss  as given to and returned by balance_loss(); None: the weights alone
       grad_losses            float32 [2]; None: ones
       dst_row                int32 [T, K] of the layout: grad_topk_weights is then float32 [rows], swiglu_grad's
-                             grad_row_weights, and each slot takes its receive row's"""
+                             grad_row_weights, and each slot takes its receive row's (0 for a row that it does not hold)"""
     return B.call_on(stream, prepare_route_grad, shape, logits, topk_idx, grad_topk_weights, balance, balance_loss,
                      grad_losses, x_active_mask, dst_row, out)

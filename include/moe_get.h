@@ -515,12 +515,20 @@ int moe_balance_loss(const moe_route_shape_t *shape, const moe_balance_t *balanc
  *  in  counts, segment_tokens from moe_balance_loss; grad_losses [2] float32 or NULL (ones)
  *  in  grad_topk_weights [T, K] float32 or NULL (the losses alone); one of it and balance is needed.  With
  *      dst_row ([T, K] from the layout; else NULL) it is moe_swiglu_grad's grad_row_weights instead: d_j =
- *      grad_topk_weights[dst_row[t, j]], 0 for slots without a row
+ *      grad_topk_weights[dst_row[t, j]], 0 for slots without a row; it has to hold every row that dst_row names
+ *      (moe_route_grad_rows is told how many rows it holds)
  *  out grad_logits [T, E] of the logits' type, 16-byte aligned */
 int moe_route_grad(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
                    const float *grad_topk_weights, const int32_t *dst_row, const uint8_t *x_active_mask,
                    const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
                    const float *grad_losses, void *grad_logits, void *stream);
+
+/* moe_route_grad through the gradients of receive rows, grad_row_weights [rows] float32: d_j = grad_row_weights[dst_row[t, j]],
+ * and 0 where dst_row[t, j] is no row of it, negative or not below rows.  dst_row is needed; everything else as there. */
+int moe_route_grad_rows(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
+                        const float *grad_row_weights, int64_t rows, const int32_t *dst_row, const uint8_t *x_active_mask,
+                        const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,
+                        const float *grad_losses, void *grad_logits, void *stream);
 
 #ifdef __cplusplus
 }
