@@ -185,6 +185,9 @@ def prepare_route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=
     S = 0
     if balance is not None:
         S, counts, tokens = balance.segments, balance_loss.counts, balance_loss.segment_tokens
+        if counts.numel() != S * E or tokens.numel() != S:
+            raise ValueError(f"balance_loss holds counts {tuple(counts.shape)} of {tokens.numel()} segments: not of these "
+                             f"{S} segments of {E} ids")
     out, out_p = _result(out, "out", logits.dtype, (T, E), (E, 1), dev)
     args = [
         ctypes.byref(shape), fp32,
@@ -210,7 +213,7 @@ def route_grad(shape, logits, topk_idx, grad_topk_weights=None, balance=None, ba
     """moe_route_grad: the gradient of the logits (of their type) through route()'s weights and balance_loss()'s losses,
     together in one pass.
       grad_topk_weights      float32 [T, K] (combine_grad's); None: the losses alone
-      balance, balance_loss  as given to and returned by balance_loss(); None: the weights alone
+      balance, balance_loss  as given to and returned by balance_loss() for this shape; None: the weights alone
       grad_losses            float32 [2]; None: ones
       dst_row                int32 [T, K] of the layout: grad_topk_weights is then float32 [rows], swiglu_grad's
                              grad_row_weights, and each slot takes its receive row's (0 for a row that it does not hold)"""
