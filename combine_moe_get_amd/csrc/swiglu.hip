@@ -8,24 +8,23 @@
 namespace moe {
 
 // The logistic function of g as a product s1 s2, and 1 - it, which is never taken as a difference.  With n = exp(-|g|) and
-// R = 1 / (1 + n) it is R for g >= 0 and n R below.  FAR: for g down to -349, where n alone may be too small for fp32 but not what
-// it multiplies: t R and t with t = exp(-|g| / 2), the square of exp(-|g| / 4), so that what stands between the two keeps its
-// digits.  Without, s2 is 1 and left out (32768 rows of 2 x 2048: forward 99 -> 95 us, gradient 114 -> 110).
+// R = 1 / (1 + n) it is R for g >= 0 and n R below.  Below kFar n alone may be too small for fp32 but not what it multiplies: there
+// it is t and t with t = exp(-|g| / 2), the square of exp(-|g| / 4), so that what stands between the two keeps its digits (R is 1
+// there).  FAR: that some g of the wave may be so far out; each is computed by its own value, whichever wave it is in.  Without, s2
+// is 1 and left out (32768 rows of 2 x 2048: forward 99 -> 95 us, gradient 114 -> 110).
+constexpr float kFar = -80.0f;
 template <bool FAR>
 struct Logistic {
   float s1, s2, rest;
   __device__ __forceinline__ Logistic(float g) {
     constexpr float kLog2e = 1.44269504088896341f;
+    const float n = __builtin_amdgcn_exp2f(fabsf(g) * -kLog2e), R = __builtin_amdgcn_rcpf(1.0f + n), nR = n * R;
+    s1 = g >= 0.0f ? R : nR;
+    rest = g >= 0.0f ? nR : R;
     if constexpr (FAR) {
-      const float q = __builtin_amdgcn_exp2f(fabsf(g) * (-0.25f * kLog2e)), t = q * q, n = t * t;
-      const float R = __builtin_amdgcn_rcpf(1.0f + n);
-      s1 = g >= 0.0f ? R : t * R;
-      s2 = g >= 0.0f ? 1.0f : t;
-      rest = g >= 0.0f ? n * R : R;
-    } else {
-      const float n = __builtin_amdgcn_exp2f(fabsf(g) * -kLog2e), R = __builtin_amdgcn_rcpf(1.0f + n), nR = n * R;
-      s1 = g >= 0.0f ? R : nR;
-      rest = g >= 0.0f ? nR : R;
+      const float q = __builtin_amdgcn_exp2f(fabsf(g) * (-0.25f * kLog2e)), t = q * q;
+      s1 = g < kFar ? t : s1;
+      s2 = g < kFar ? t : 1.0f;
     }
   }
   __device__ __forceinline__ float scaled(float x) const { return FAR ? x * s2 : x; }
@@ -35,7 +34,7 @@ __device__ __forceinline__ bool far_out(const float *g) {
   float least = g[0];
 #pragma unroll
   for (int e = 1; e < 8; ++e) least = fminf(least, g[e]);
-  return ballot(least < -80.0f) != 0;
+  return ballot(least < kFar) != 0;
 }
 
 __device__ __forceinline__ uint32_t pack2s(float a, float b) {
