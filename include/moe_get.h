@@ -400,7 +400,8 @@ int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, con
                      float *grad_v, void *stream);
 
 /* The gate between the two products of a layer that trains: row r of h0 holds [g | u], 2 * features elements, and
- *   out[r, i] = row_weights[r] silu(g_i) u_i        (row_weights NULL: ones), in fp32, rounded once to bf16.
+ *   out[r, i] = row_weights[r] silu(g_i) u_i        (row_weights NULL: ones), in fp32, rounded once to bf16 (for g below -80,
+ * where the logistic function alone may be too small for fp32, in 64 bits).
  * With the routing weights here (moe_dispatch's expand_weights) the combine takes ones, and its backward pass does
  * not need the experts' results: moe_swiglu_grad gives the weights' gradient.
  * For the backward pass h0 may be kept in 8 bits (a checkpoint): codes and scales, both NULL or both given.  Each half
@@ -425,7 +426,7 @@ int moe_swiglu(int64_t rows, int32_t features, const uint16_t *h0, const float *
  *   grad_h0[r] = [ w d u s (1 + g (1 - s)) | w d g s ], grad_row_weights[r] = sum_i d_i g_i s_i u_i,
  *   out[r] = w g s u: the forward's result again, for the second product's weight gradient (from a checkpoint: of the
  *   values that it holds).
- * fp32 throughout, bf16 results rounded once.  Every output may be NULL and is then not computed (not all of them).
+ * fp32 throughout (64 bits for g below -80), bf16 results rounded once.  Every output may be NULL and is then not computed (not all of them).
  *  in  grad_out [rows, features] bf16
  *  out grad_h0 [rows, 2 * features] bf16, out [rows, features] bf16, grad_row_weights [rows] float32 */
 int moe_swiglu_grad(int64_t rows, int32_t features, const uint16_t *grad_out, const uint16_t *h0, const int8_t *codes,
