@@ -152,15 +152,15 @@ __global__ void __launch_bounds__(256) balance_sums_kernel(BalanceArgs a, int sl
     BalanceSpace ws;
     if (!ALONE) ws = balance_space(a.ws, slices, E, a.S);
     for (int e = threadIdx.x; e < E; e += 256) {
-      float v = red[0][e];
+      double v = (double)red[0][e];  // of at most 64 tokens each
 #pragma unroll
-      for (int k = 1; k < TOKENS; ++k) v += red[k][e];
+      for (int k = 1; k < TOKENS; ++k) v += (double)red[k][e];
       if constexpr (ALONE) {
-        a.sums[(int64_t)g * E + e] = v;
+        a.sums[(int64_t)g * E + e] = (float)v;
         a.counts[(int64_t)g * E + e] = cnt[e];
-        loss += f * cnt[e] * (double)v;
+        loss += f * cnt[e] * v;
       } else {
-        ws.sum[(int64_t)blockIdx.x * E + e] = v;
+        ws.sum[(int64_t)blockIdx.x * E + e] = (float)v;
         ws.cnt[(int64_t)blockIdx.x * E + e] = cnt[e];
       }
     }

@@ -497,8 +497,8 @@ size_t moe_balance_workspace_size(const moe_route_shape_t *shape, const moe_bala
 /*  in  logits, x_active_mask as for moe_route; topk_idx [T, K]: ids outside [0, E) are not counted
  *  out losses [2] float32, counts [segments, E] int32, prob_sums [segments, E] float32, segment_tokens [segments] int32
  *  workspace  16-byte aligned; calls that overlap need one each
- * Of the shape, num_groups, topk_groups, group_score, renormalize and scale do not matter.  Sums of a few tokens' p in fp32,
- * then in 64 bits, in an order that the sizes fix. */
+ * Of the shape, num_groups, topk_groups, group_score, renormalize and scale do not matter.  Sums of at most 64 tokens' p in fp32,
+ * then in 64 bits (a workgroup's rounded to fp32 between the two launches), in an order that the sizes fix. */
 int moe_balance_loss(const moe_route_shape_t *shape, const moe_balance_t *balance, int32_t logits_fp32,
                      const void *logits, const int32_t *topk_idx, const uint8_t *x_active_mask, float *losses,
                      int32_t *counts, float *prob_sums, int32_t *segment_tokens, void *workspace,
