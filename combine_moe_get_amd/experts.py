@@ -20,9 +20,10 @@ ROWS_BF16, ROWS_INT8, ROWS_MXFP4 = 0, 1, 2
 ACT_NONE, ACT_SWIGLU = 0, 1
 EXPERTS_FORWARD, EXPERTS_DGRAD, EXPERTS_WGRAD = 0, 1, 2
 
-# a device's current stream as a hipStream_t, and the current device; a process that calls them has tensors on one
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+# a device's current stream as a hipStream_t, and the current device: without the objects that torch.cuda makes of them, where
+# torch has these names (a build without has torch.cuda's)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or (lambda: torch.cuda.current_device())
 
 _TYPE_OF = {torch.bfloat16: ROWS_BF16, torch.int8: ROWS_INT8, torch.uint8: ROWS_MXFP4}
 U8 = (torch.uint8,)
