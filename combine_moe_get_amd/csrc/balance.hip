@@ -4,9 +4,13 @@
 //   balance = coef / S sum_g E / (K T_g^2) sum_e c_e P_e,   z = z_coef / T sum_t lse_t^2,
 // and back: dbalance / dp_te = A_e = coef E c_e / (S K T_g^2), so of log s it is p_e (A_e - sum_f A_f p_f); through the weights
 // a_j (see moe_route_grad); of l: the same for softmax, times 1 - s_e for sigmoids; z adds 2 z_coef lse / T softmax(l).
-// Both read the logits once.  Bound by instructions (two exponentials or an exponential and a reciprocal an id) and, below some
-// 4000 tokens, by launches: 16384 tokens of 256 in 64 segments, sigmoids: sums 10.3 us (17 MB), losses 5.0, gradient 13 (34 MB;
-// 6.7 at a copy's rate); 4096 of 64 in bf16: 4.6, 5.3, 4.6.
+// Both read the logits once.  The gradient is bound by instructions (two exponentials or an exponential and a reciprocal an id:
+// vector instructions in 79% of the cycles at 16384 tokens of 256, 97 at 65536), the sums by how few tokens are under way (44%, 75%)
+// and, below some 4000 tokens, both by launches: 16384 tokens of 256 in 64 segments, sigmoids: sums 10.3 us (17 MB), losses 5.0,
+// gradient 13.5 (34 MB; 6.7 at a copy's rate); 4096 of 64 in bf16: 4.7, 5.3, 4.7.
+// Where a reciprocal is the instruction's (of a sum of scores, of a segment's tokens, in the sigmoid) it is good to one step of fp32,
+// 2^-23: sigmoids to 2.1 steps, their p to 3.1 of 2048 ids, those of softmax to 3 and half a step for each 1 that the logit is below
+// the largest (measured).  The weights' sum is divided by, as in the choice: there a remnant of 1 - w would stand for 0.
 #include "route_internal.hpp"
 
 namespace moe {

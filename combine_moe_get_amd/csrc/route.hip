@@ -8,10 +8,18 @@
 // 9 of 256 do (K = 8).  Each of those is computed in 64 bits by a lane of its own and compared with the others, at once and not
 // in rounds of one best after the other.  Groups whose 32-bit scores are too near at the border, and rows of so many equal values
 // that the candidates do not fit, go a longer way in 64 bits.
-// Bound by instructions (538 a wave of two tokens, with groups) and, up to some 4000 tokens, by the launch: 16384 tokens of 256
-// fp32 logits 7.4 us (17 MB; at a copy's rate 3.3, and 2.9 for the launch), with four of eight groups 9.5, sigmoids with a bias
-// and the groups' two best 18; 128 tokens 3.8, 4.7, 6.2.  By rounds, in 64 bits: 16384 tokens with groups 30 us on a wave a token,
-// 13 on 16 lanes.
+// Many tokens are bound by instructions (with a bias and the groups' two best 937 a wave of two tokens: vector instructions in 80% of
+// the cycles at 16384 tokens, in all at 65536; with groups alone 538, 71%), up to some 4000 by the launch and by the chain of folds,
+// LDS and 64-bit steps of the one wave that a SIMD has (44% with the bias at 4096): 16384 tokens of 256 fp32 logits 7.4 us (17 MB;
+// at a copy's rate 3.3, and 2.9 for the launch), with four of eight groups 9.5, sigmoids with a bias and the groups' two best 18;
+// 128 tokens 3.8, 4.7, 6.2.  By rounds, in 64 bits: 16384 tokens with groups 30 us on a wave a token, 13 on 16 lanes.
+// How many go the longer way depends on the logits, since the error of a key in 32 bits is known as 2^-21 + 2^-23 of it: scores
+// below some 1e-6 look alike unless a bias sets them apart.  16384 tokens of 256, us, for softmax logits of deviation 1 / 5 / 10 / 15
+// and sigmoids around 0 / -8 / -12 / -16:
+//   groups by two, no bias      12 / 13 / 17 / 19     11 / 14 / 19 / 20
+//   a bias of zeros             16 / 24 / 37 / 45     12 / 12 / 12 / 43
+//   both                        22 / 38 / 64 / 69     15 / 18 / 24 / 69
+//   a bias of deviation 0.1     18 / 18 / 18 / 18     17 / 15 / 15 / 15
 #include "route_internal.hpp"
 
 namespace moe {
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(256) route_kernel(RouteArgs a) {
       kept |= token_bits<L>(ballot(in)) << g0;
     }
     lds_order();
-    if (ballot(open))  // two groups too near one another at the border: some of 10^5 tokens
+    if (ballot(open))  // two groups too near one another at the border: few tokens while scores are far above 2^-21
       kept = groups_wide<L, NV>(a, lane, my.cand, [&](int i) {
         const int id = id_of<L>(lane, i);
         return BIAS ? key_of(l[i], id) : l[i] > nonef ? score(l[i]) : none;

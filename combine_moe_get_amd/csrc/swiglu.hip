@@ -84,7 +84,7 @@ constexpr uint64_t kMostGroups = 1 << 20;  // of a launch; they walk what is lef
 // ---- forward: 16 lanes a block of 128 columns of a row, 8 of each half a lane -----------------------
 //
 // One pass, bound by memory: 32768 rows of 2 x 2048 with codes 90 us (541 MB, 6.0 TB/s; a large copy reaches 5.1), without 68
-// (403 MB, 5.9 TB/s).  A thread's 16 values take 284 vector instructions, in 79% of those cycles; with codes clamped and packed
+// (403 MB, 5.9 TB/s).  A thread's 16 values take 285 vector instructions, in 80% of those cycles; with codes clamped and packed
 // one by one, divisions for the reciprocals and 64 bits of address a thread it was these, 467, that bound it (108 us).  Stores
 // go past the caches: 116 and 85 us where they do not, the gradient 159 for 155 (all before the instructions were fewer).  Two
 // blocks a thread took 107 for 105 us, and 4.8 for 3.8 on 400 rows of 2 x 512.

@@ -444,9 +444,11 @@ int moe_swiglu_grad(int64_t rows, int32_t features, const uint16_t *grad_out, co
  * the only atomics count integers.
  *
  * Speed, us of the kernels in a graph (some 3 of them each launch): 256 fp32 logits a token, 8 chosen; 128 / 4096 / 65536 tokens:
- * moe_route 3.8 / 4.2 / 22, with four of eight groups 4.7 / 5.3 / 29, with a bias and the groups' two best 6.2 / 7.0 / 49;
- * moe_balance_loss 10 / 12 / 36 (one launch up to some 32 tokens of 256 or 128 of 64, else two); moe_route_grad 4.8 / 5.8 / 39.
- * A number of ids that is a multiple of four is read four at a time; rows of equal logits take the longest. */
+ * moe_route 3.8 / 4.8 / 24, with four of eight groups 4.8 / 5.9 / 30, with a bias and the groups' two best 6.5 / 8.2 / 51;
+ * moe_balance_loss 9 / 12 / 36 (one launch up to some 32 tokens of 256 or 128 of 64, else two); moe_route_grad 4.3 / 6.0 / 41.
+ * A number of ids that is a multiple of four is read four at a time.  With a bias, or groups by two, the choice's time depends on the
+ * logits: scores below some 1e-6 that no bias sets apart are told apart the longer way.  16384 tokens of 256 with a bias of zeros:
+ * softmax of logits of deviation 1 / 5 / 10 16 / 24 / 37, sigmoids around 0 / -16 12 / 43; rows of equal logits take the longest. */
 typedef struct moe_route_shape {
   int32_t num_tokens;   /* T: 0 <= T < 2^24 */
   int32_t num_ids;      /* E: 1..2048 */
