@@ -154,11 +154,12 @@ int moe_route_grad_rows(const moe_route_shape_t *shape, int32_t logits_fp32, con
   const int st = check_shape(shape);
   if (st != MOE_OK) return st;
   if (rows < 0) return MOE_ERR_SHAPE;
+  if (rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   if (shape->num_tokens > 0 && (!dst_row || (rows > 0 && !grad_row_weights))) return MOE_ERR_ARG;
   // without rows there is nothing to read, and the slots' gradients are zeros
   const float *g = rows > 0 ? grad_row_weights : (const float *)dst_row;
-  return route_grad(shape, logits_fp32, logits, topk_idx, g, rows < INT32_MAX ? (int32_t)rows : INT32_MAX, dst_row,
-                    x_active_mask, balance, counts, segment_tokens, grad_losses, grad_logits, stream);
+  return route_grad(shape, logits_fp32, logits, topk_idx, g, (int32_t)rows, dst_row, x_active_mask, balance, counts,
+                    segment_tokens, grad_losses, grad_logits, stream);
 }
 
 }  // extern "C"

@@ -527,7 +527,8 @@ int moe_route_grad(const moe_route_shape_t *shape, int32_t logits_fp32, const vo
                    const float *grad_losses, void *grad_logits, void *stream);
 
 /* moe_route_grad through the gradients of receive rows, grad_row_weights [rows] float32: d_j = grad_row_weights[dst_row[t, j]],
- * and 0 where dst_row[t, j] is no row of it, negative or not below rows.  dst_row is needed; everything else as there. */
+ * and 0 where dst_row[t, j] is no row of it, negative or not below rows (0 <= rows < 2^31).  dst_row is needed; everything else as
+ * there. */
 int moe_route_grad_rows(const moe_route_shape_t *shape, int32_t logits_fp32, const void *logits, const int32_t *topk_idx,
                         const float *grad_row_weights, int64_t rows, const int32_t *dst_row, const uint8_t *x_active_mask,
                         const moe_balance_t *balance, const int32_t *counts, const int32_t *segment_tokens,

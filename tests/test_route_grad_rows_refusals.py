@@ -48,3 +48,7 @@ def test_the_binding_gives_the_rows_that_there_are(rows, monkeypatch):
     assert c._fn is experts._lib().moe_route_grad and len(c._args) == 13
     with pytest.raises(ValueError):
         mg.prepare_route_grad(s, l, ids, torch.zeros(rows), dst_row=torch.zeros(7, dtype=torch.int32))
+
+
+def test_more_rows_than_a_map_can_name():
+    assert call(rows=2 ** 31) == -4 and call(rows=2 ** 62) == -4 and call(T=0, rows=2 ** 31) == -4
