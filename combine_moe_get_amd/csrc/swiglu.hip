@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(256) swiglu_grad_kernel(SwigluArgs a) {
             du[e] = act * wd;
             dg[e] = s.s * u[e] * wd * __builtin_fmaf(g[e], s.rest, 1.0f);
             h[e] = hu * w;
-            dot = __builtin_fmaf(d[e], g[e] < kFar ? 0.0f : hu, dot);
+            const float sum = __builtin_fmaf(d[e], hu, dot);
+            dot = g[e] < kFar ? dot : sum;
           }
           if (__builtin_expect(far_out(g), 0)) {  // one element after the other: unrolled it takes 126 registers for 84
             f32x8 gx, ux, dx, dgx, dux, hx;

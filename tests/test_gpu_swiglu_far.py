@@ -68,3 +68,22 @@ def test_lowest_values():
     g = b.grad_h0.cpu()
     assert g[0, 0] == 0 and g[0, 8] == 0 and g[1, 0].isnan() and g[1, 8].isnan()
     assert torch.equal(torch.nan_to_num(b.out.cpu(), nan=7.0), torch.nan_to_num(f, nan=7.0))
+
+
+def test_infinite_factors():
+    """An infinite gradient or u beside a small logistic function: infinities, as the products are, and no NaN."""
+    inf = float("inf")
+    g = [-79.0, -81.0, -100.0, -150.0]
+    h0 = torch.ones(8, 16, dtype=torch.bfloat16)
+    d = torch.ones(8, 8, dtype=torch.bfloat16)
+    for k, v in enumerate(g):
+        h0[k, 3], h0[4 + k, 3] = v, v
+        d[k, 3] = inf
+        h0[4 + k, 11] = inf
+    w = torch.ones(8, device=X.DEV)
+    b = mg.swiglu_grad(d.to(X.DEV), h0.to(X.DEV), row_weights=w)
+    gw, gr, out = b.grad_row_weights.cpu(), b.grad_h0.cpu(), b.out.cpu()
+    assert (gw == -inf).all()
+    assert (gr[:4, 3] == -inf).all() and (gr[:4, 11] == -inf).all() and (gr[4:, 3] == -inf).all()
+    assert (out[4:, 3] == -inf).all() and bool(out[:4].isfinite().all())
+    assert torch.equal(mg.swiglu(h0.to(X.DEV), w).out.cpu(), out)
