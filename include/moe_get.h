@@ -403,7 +403,8 @@ int moe_combine_grad(const moe_get_shape_t *shape, const uint16_t *grad_out, con
  *   out[r, i] = row_weights[r] silu(g_i) u_i        (row_weights NULL: ones), in fp32, rounded once to bf16 (for g below -80,
  * where the logistic function alone may be too small for fp32, in 64 bits).
  * With the routing weights here (moe_dispatch's expand_weights) the combine takes ones, and its backward pass does
- * not need the experts' results: moe_swiglu_grad gives the weights' gradient.
+ * not need the experts' results: moe_swiglu_grad gives the weights' gradient.  (Slots of copy and constant experts have no
+ * row: their weights act in the combine alone, so a layer with such experts keeps all weights there.)
  * For the backward pass h0 may be kept in 8 bits (a checkpoint): codes and scales, both NULL or both given.  Each half
  * of a row is cut into blocks of 128 elements (the last may be shorter).  Per block dyn = 127 (1 / amax), scale = 1 / dyn,
  * code = round-half-even(x dyn) in [-127, 127], each operation rounded once to binary32 (amax 0: codes 0, scale 0; NaN
