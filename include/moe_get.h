@@ -425,8 +425,8 @@ int moe_swiglu(int64_t rows, int32_t features, const uint16_t *h0, const float *
 /* Gradient of moe_swiglu, from h0 or from its checkpoint (one of the two, the other NULL).  With d = grad_out[r],
  * w = row_weights[r] and s = 1 / (1 + exp(-g)):
  *   grad_h0[r] = [ w d u s (1 + g (1 - s)) | w d g s ], grad_row_weights[r] = sum_i d_i g_i s_i u_i,
- *   out[r] = w g s u: the forward's result again, for the second product's weight gradient (from a checkpoint: of the
- *   values that it holds).
+ *   out[r] = w g s u: the forward's result again, bit for bit from h0, for the second product's weight gradient (from a
+ *   checkpoint: of the values that it holds).
  * fp32 throughout (64 bits for g below -80), bf16 results rounded once.  Every output may be NULL and is then not computed (not all of them).
  *  in  grad_out [rows, features] bf16
  *  out grad_h0 [rows, 2 * features] bf16, out [rows, features] bf16, grad_row_weights [rows] float32 */
